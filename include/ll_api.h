@@ -355,6 +355,195 @@ ll_status ll_kv_recache(const ll_kvcache* cache, const void* x, int d_model,
                         const long long* slot_frames, int n_slots, const ll_rope_desc* rope,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ==========================================================================
+ * Streams of single tokens
+ *
+ * The entry points above work on whole latent frames of one stream. The ones
+ * below do the same path (rotate, append, attend) at the grain of single
+ * tokens, for a ragged batch of sequences whose keys and values live in pages
+ * of one shared pool, with heads of K and V shared by groups of query heads.
+ * The conventions at the top of this file hold here too; token tensors are
+ * [rows][heads][D] with D fastest, heads D apart, and a row stride in elements
+ * that the caller gives (a multiple of 8, at least heads * D), so that q, k and
+ * v may be slices of one fused projection.
+ * ========================================================================== */
+
+#define LL_MAX_TOKEN_HEADS 128  /* query heads of ll_paged_attention */
+#define LL_MAX_TOKEN_PAIRS 64   /* rotated pairs of a head */
+
+typedef enum ll_rope_layout {
+  LL_ROPE_INTERLEAVED = 0,  /* pair i is (x[2i], x[2i+1]) */
+  LL_ROPE_HALF = 1          /* pair i is (x[i], x[i + rot_dim/2]) */
+} ll_rope_layout;
+
+/*
+ * Rotary embedding of token positions: the first rot_dim elements of a head
+ * are rot_dim/2 pairs; pair i of a token at position p is turned by the angle
+ * p * w_i and multiplied by `amplitude`; the other elements pass unchanged.
+ * turns[i] is w_i / (2 pi), the turn per position, as a fraction of 2^64
+ * (turns of a position are then an exact product modulo one turn, at any
+ * position a 32-bit integer holds). Fill it with ll_token_rope_init, or set
+ * turns[] yourself for other frequency schemes.
+ */
+typedef struct ll_token_rope_desc {
+  int rot_dim;       /* a multiple of 16, at most 2 * LL_MAX_TOKEN_PAIRS and D */
+  int layout;        /* ll_rope_layout */
+  float amplitude;   /* finite; 1 for a plain rotation */
+  int reserved;      /* 0 */
+  uint64_t turns[LL_MAX_TOKEN_PAIRS];
+} ll_token_rope_desc;
+
+/*
+ * Fills *desc (host only, no GPU needed). w_i = theta0^(-2i/rot_dim) * f_i with
+ *   f_i = r_i + (1 - r_i) * scale,
+ *   r_i = clamp((original_len * w'_i / (2 pi) - beta_slow) / (beta_fast - beta_slow), 0, 1),
+ * w'_i the unscaled frequency: pairs that turn beta_fast times or more within
+ * the length a model was trained at (original_len) keep their frequency, those
+ * that turn beta_slow times or less are interpolated by `scale`, those between
+ * get a mixture (interpolation by parts; Peng et al. 2023, "YaRN"). original_len
+ * 0 interpolates every pair by `scale` (position interpolation, the t_scale of
+ * ll_rope_desc; 1: plain rotary embedding).
+ * Errors: LL_ERR_INVALID_ARG for desc NULL, a rot_dim that is no positive
+ * multiple of 16 up to 2 * LL_MAX_TOKEN_PAIRS, an unknown layout, theta0 not
+ * finite or <= 1, scale outside (0, 1], original_len negative or not finite,
+ * beta_fast <= beta_slow or beta_slow < 0 or not finite where original_len > 0,
+ * an amplitude that is not finite.
+ */
+ll_status ll_token_rope_init(ll_token_rope_desc* desc, int rot_dim, int layout, double theta0, double scale,
+                             double original_len, double beta_fast, double beta_slow, double amplitude);
+
+/*
+ * out[t][h] = R(positions[t]) x[t][h] for T tokens of H heads (dtype F32 or
+ * BF16, computed in fp32, rounded once), or R(positions[t])^T x[t][h] when
+ * `transpose` is non-zero: the gradient of the rotation, which for amplitude 1
+ * also undoes it. positions: DEVICE int32 [T], any value. out may be x (with
+ * the same stride); other overlaps give undefined results. T = 0 is a no-op.
+ * Errors: LL_ERR_INVALID_ARG for NULL or misaligned (16 bytes; positions 4)
+ * pointers, T < 0, H < 1, D not a multiple of 16 or < rot_dim, a stride that is
+ * no multiple of 8 or < H * D, another dtype, an invalid descriptor;
+ * LL_ERR_UNSUPPORTED for D > 1024 or H * D >= 2^24.
+ */
+ll_status ll_token_rope_apply(const void* x, long long x_stride, void* out, long long out_stride, ll_dtype dtype,
+                              const int32_t* positions, int T, int H, int D, const ll_token_rope_desc* rope,
+                              int transpose, void* stream);
+
+/*
+ * A pool of pages (caller-owned device memory), one layer's.
+ * k, v: [n_pages][H][page_size][D] of `dtype` (BF16 or FP8_E4M3): the tokens of
+ * one page and head lie together.
+ * k_scale, v_scale: [n_pages][H] fp32, FP8 only (NULL otherwise): one scale for
+ * each block of page_size tokens and head; value = decode(code) * scale.
+ * page_size: 16, 32, 64 or 128; D: 64 or 128; 16-byte aligned k and v.
+ */
+typedef struct ll_paged_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  ll_dtype dtype;
+  int n_pages, page_size;
+  int H, D;          /* heads of K and V */
+} ll_paged_cache;
+
+/*
+ * The tokens of one call: sequence b has the rows [q_start[b], q_start[b+1]) of
+ * the token tensors, which are its LAST tokens: row i of them stands at
+ * position kv_len[b] - (q_start[b+1] - q_start[b]) + i, and kv_len[b] counts
+ * the sequence's tokens with these included. Token t of sequence b lives in
+ * page page_table[b][t / page_size], row t % page_size of it.
+ * q_start [B+1] (ascending, from 0 on), kv_len [B], page_table [B][max_pages]
+ * are DEVICE int32 arrays, read when the call runs; max_q and max_kv are the
+ * host's bounds on the rows and the length of a sequence.
+ * What the arrays say is bounded on the device: rows from max_q on and rows
+ * beyond total_q are not processed; keys beyond max_kv or max_pages * page_size
+ * do not exist; an entry of page_table outside [0, n_pages) names no page (its
+ * keys do not exist, tokens appended there are dropped), so pages that no query
+ * sees any more may be given back and their entries set to -1. Rows of no
+ * sequence are left as they are.
+ */
+typedef struct ll_token_batch {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int B, max_pages;
+  int total_q;       /* rows of the token tensors */
+  int max_q, max_kv;
+} ll_token_batch;
+
+/*
+ * Writes the batch's tokens into their pages. k, v: [total_q][H][D] BF16 with
+ * row strides k_stride, v_stride. K is rotated with `rope` at its token's
+ * position first (rope NULL: stored as given).
+ * BF16 pool: values rounded once. FP8 pool: the scale of a touched (page, head)
+ * becomes s = max(s_old, the smallest power of two with 448 s >= max|x| over the
+ * page's new tokens), s_old being the stored scale where the page holds earlier
+ * tokens of the sequence (new tokens do not begin at its row 0) and 0 otherwise;
+ * new codes are RNE(x / s) saturated (0 where s is 0), and where s grew over
+ * s_old the earlier tokens' codes become RNE(code * s_old / s). Powers of two
+ * make that re-coding exact but for underflow: a page filled token by token
+ * carries one rounding, like one that is written at once. max|x| is taken over
+ * finite values: infinities saturate, NaN stays NaN. Rows of a page behind the
+ * sequence's last token are left as they are.
+ * The pages written must differ between the sequences of a call.
+ * Errors: LL_ERR_INVALID_ARG for NULL or misaligned pointers (k, v 16 bytes,
+ * arrays 4), an invalid cache or batch descriptor, strides that are no multiple
+ * of 8 or < H * D, an in_dtype other than BF16, an invalid rope descriptor or
+ * rot_dim > D.
+ */
+ll_status ll_paged_append(const ll_paged_cache* cache, const ll_token_batch* batch, const void* k, long long k_stride,
+                          const void* v, long long v_stride, ll_dtype in_dtype, const ll_token_rope_desc* rope,
+                          void* stream);
+
+/*
+ * What happens to a score and which keys a query sees (NULL: plain causal).
+ * The score of query position p and key position j, head h:
+ *   x = softmax_scale * q . k   (softmax_scale 0 means 1/sqrt(D))
+ *   x = soft_cap * tanh(x / soft_cap)   where soft_cap > 0
+ *   x = x - slopes[h] * |p - j|         where slopes != NULL
+ * Key j exists for j < kv_len[b] (see ll_token_batch) and is seen when
+ *   j < prefix_len[b], or j <= p and (window == 0 or p - j < window or j < n_sink):
+ * `window` most recent tokens plus n_sink pinned first ones (the frame sink and
+ * short window, at the grain of tokens), and a prefix whose tokens see each other.
+ * prefix_len: DEVICE int32 [B] or NULL. slopes: HOST float [Hq] or NULL.
+ */
+typedef struct ll_score_desc {
+  float softmax_scale;
+  float soft_cap;
+  int window, n_sink;
+  const int32_t* prefix_len;
+  const float* slopes;
+} ll_score_desc;
+
+/*
+ * out = softmax(scores) V for the batch's rows, over the pool that already holds
+ * them (append first). q, out: [total_q][Hq][D] BF16; Hq a multiple of the
+ * pool's H, query head h reads K/V head h / (Hq / H). q is rotated at its
+ * positions when rope != NULL. out rows are contiguous (stride Hq * D).
+ * A row that sees no key gets 0, and -inf in lse. lse (optional): [total_q][Hq]
+ * fp32, natural-log sum of exp of the final scores.
+ * Keys that no query of a tile of rows sees are not read, so what their places
+ * hold does not matter; a NaN or infinity in a key or value that some query of
+ * the call sees may spoil the call's other rows of that sequence too.
+ * Over a BF16 pool the rotated q and the softmax weights are rounded to bf16;
+ * over an FP8 pool codes are used exactly, q and weights are rounded to fp16
+ * under a power-of-two scale. Sums, maxima and outputs before the last rounding
+ * are fp32.
+ * workspace: ll_paged_attention_workspace_bytes() bytes (NULL allowed when 0),
+ * uninitialised, 16-byte aligned; calls that share it must be ordered.
+ * Errors: LL_ERR_INVALID_ARG for NULL or misaligned pointers, an invalid cache,
+ * batch or rope descriptor, a q_dtype other than BF16, Hq not a multiple of H,
+ * a q_stride that is no multiple of 8 or < Hq * D, a negative or non-finite
+ * softmax_scale or soft_cap, negative window or n_sink, a slope that is not
+ * finite, a workspace that is too small; LL_ERR_UNSUPPORTED for Hq >
+ * LL_MAX_TOKEN_HEADS or H * B > 2^20.
+ */
+size_t ll_paged_attention_workspace_bytes(const ll_paged_cache* cache, const ll_token_batch* batch, int Hq);
+
+ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype, int Hq,
+                             const ll_paged_cache* cache, const ll_token_batch* batch,
+                             const ll_token_rope_desc* rope, const ll_score_desc* scores, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libll_swa.so")
 LL_OK, LL_ERR_INVALID_ARG, LL_ERR_UNSUPPORTED, LL_ERR_CUDA, LL_ERR_TIMEOUT = range(5)
 LL_F32, LL_BF16, LL_FP8_E4M3 = 0, 1, 2
 MAX_HEADS = 64
+LL_ROPE_INTERLEAVED, LL_ROPE_HALF = 0, 1
+MAX_TOKEN_HEADS, MAX_TOKEN_PAIRS = 128, 64
 ABI_VERSION = 2
 
 EXPORTED = (
@@ -30,6 +32,8 @@ EXPORTED = (
     "ll_append_and_attend_workspace_bytes", "ll_append_and_attend", "ll_phase_coherence",
     "ll_selftest_bounded_waits", "ll_sink_window_attention_fp8_mma_workspace_bytes",
     "ll_sink_window_attention_fp8_mma",
+    "ll_token_rope_init", "ll_token_rope_apply", "ll_paged_append", "ll_paged_attention_workspace_bytes",
+    "ll_paged_attention",
 )
 NOALLOC_SCRATCH_BYTES = 48 * 1024 * 1024
 
@@ -52,6 +56,28 @@ class KVCacheC(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int),
                 ("D", ctypes.c_int), ("tokens_per_frame", ctypes.c_int), ("n_sink", ctypes.c_int),
                 ("n_local", ctypes.c_int)]
+
+
+class TokenRopeDescC(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int), ("turns", ctypes.c_uint64 * MAX_TOKEN_PAIRS)]
+
+
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int)]
+
+
+class TokenBatchC(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("max_pages", ctypes.c_int), ("total_q", ctypes.c_int), ("max_q", ctypes.c_int),
+                ("max_kv", ctypes.c_int)]
+
+
+class ScoreDescC(ctypes.Structure):
+    _fields_ = [("softmax_scale", ctypes.c_float), ("soft_cap", ctypes.c_float), ("window", ctypes.c_int),
+                ("n_sink", ctypes.c_int), ("prefix_len", ctypes.c_void_p), ("slopes", ctypes.POINTER(ctypes.c_float))]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -87,6 +113,13 @@ def lib() -> ctypes.CDLL:
         L.ll_append_and_attend.argtypes = [cp, vp, vp, vp, i, ll_, i, rp, f, vp, vp, vp, sz, vp]
         L.ll_phase_coherence.argtypes = [rp, i, ll_, i, vp, vp]
         L.ll_selftest_bounded_waits.argtypes = [vp]
+        tr, pc, tb = (ctypes.POINTER(c) for c in (TokenRopeDescC, PagedCacheC, TokenBatchC))
+        L.ll_token_rope_init.argtypes = [tr, i, i, d, d, d, d, d, d]
+        L.ll_token_rope_apply.argtypes = [vp, ll_, vp, ll_, i, vp, i, i, i, tr, i, vp]
+        L.ll_paged_append.argtypes = [pc, tb, vp, ll_, vp, ll_, i, tr, vp]
+        L.ll_paged_attention_workspace_bytes.argtypes = [pc, tb, i]
+        L.ll_paged_attention_workspace_bytes.restype = sz
+        L.ll_paged_attention.argtypes = [vp, ll_, i, i, pc, tb, tr, ctypes.POINTER(ScoreDescC), vp, vp, vp, sz, vp]
         for name in EXPORTED[2:]:
             if not name.endswith("_workspace_bytes"):
                 getattr(L, name).restype = i
@@ -410,3 +443,200 @@ def selftest_bounded_waits(stream=None) -> int:
     the device error code it leaves (read and cleared by ll_device_error)."""
     _check(lib().ll_selftest_bounded_waits(_stream(stream)))
     return device_error(stream)
+
+
+# ---------------------------------------------------------------------------
+# Streams of single tokens: rotary positions, a paged pool of keys and values,
+# and attention of a ragged batch of sequences over it.
+# ---------------------------------------------------------------------------
+class TokenRope:
+    """Rotary embedding of token positions (mirrors ll_token_rope_desc; ll_token_rope_init fills it).
+
+    The first rot_dim elements of a head are turned; layout "half" pairs element
+    i with i + rot_dim / 2, "interleaved" 2i with 2i + 1. scale < 1 interpolates
+    positions, by parts where original_len is given (beta_fast, beta_slow: turns
+    within original_len from which on a pair keeps its frequency, and up to
+    which it is interpolated in full); rotated elements are multiplied by
+    amplitude.
+    """
+
+    def __init__(self, rot_dim: int, theta0: float = 10000.0, layout: str = "half", scale: float = 1.0,
+                 original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, amplitude: float = 1.0):
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+        self.rot_dim, self.layout = rot_dim, layout
+        self._c = TokenRopeDescC()
+        _check(lib().ll_token_rope_init(self._c, rot_dim, LL_ROPE_HALF if layout == "half" else LL_ROPE_INTERLEAVED,
+                                        theta0, scale, original_len, beta_fast, beta_slow, amplitude))
+
+    def to_c(self) -> TokenRopeDescC:
+        return self._c
+
+
+class PagedKVCache:
+    """One layer's pool of pages in device memory (mirrors ll_paged_cache):
+    k, v [n_pages, H, page_size, D]; an "fp8" pool has k_scale, v_scale [n_pages, H]."""
+
+    def __init__(self, n_pages: int, page_size: int, H: int, D: int, dtype: str = "bf16", device: str = "cuda"):
+        self.n_pages, self.page_size, self.H, self.D, self.dtype = n_pages, page_size, H, D, dtype
+        shape = (n_pages, H, page_size, D)
+        tdt = {"bf16": torch.bfloat16, "fp8": torch.uint8}[dtype]
+        self.k = torch.zeros(shape, dtype=tdt, device=device)
+        self.v = torch.zeros(shape, dtype=tdt, device=device)
+        self.k_scale = self.v_scale = None
+        if dtype == "fp8":
+            self.k_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
+            self.v_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
+        self.code = LL_FP8_E4M3 if dtype == "fp8" else LL_BF16
+
+    def to_c(self) -> PagedCacheC:
+        fp8 = self.k_scale is not None
+        return PagedCacheC(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr() if fp8 else None,
+                           self.v_scale.data_ptr() if fp8 else None, self.code, self.n_pages, self.page_size, self.H,
+                           self.D)
+
+
+class TokenBatch:
+    """Which tokens of which sequences a call works on (mirrors ll_token_batch).
+
+    q_start [B+1], kv_len [B], page_table [B, max_pages]: contiguous int32 CUDA
+    tensors, read on the device when a call runs, so their contents may change
+    between calls (and between replays of a captured graph) as long as max_q and
+    max_kv still bound them.
+    """
+
+    def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_q: int, max_kv: int):
+        if page_table.dim() != 2:
+            raise ValueError(f"page_table must be [B, max_pages], got shape {tuple(page_table.shape)}")
+        B, max_pages = page_table.shape
+        _expect(page_table, (B, max_pages), torch.int32, "page_table")
+        _expect(q_start, (B + 1,), torch.int32, "q_start")
+        _expect(kv_len, (B,), torch.int32, "kv_len")
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.B, self.max_pages, self.max_q, self.max_kv = B, max_pages, int(max_q), int(max_kv)
+
+    def to_c(self, total_q: int) -> TokenBatchC:
+        return TokenBatchC(_ptr(self.q_start), _ptr(self.kv_len), _ptr(self.page_table), self.B, self.max_pages,
+                           total_q, self.max_q, self.max_kv)
+
+
+class Scores:
+    """What happens to scores and which keys are seen (mirrors ll_score_desc): see paged_attention.
+
+    prefix_len: int32 CUDA tensor [B]; slopes: one float per query head.
+    """
+
+    def __init__(self, softmax_scale: float = 0.0, window: int = 0, n_sink: int = 0,
+                 prefix_len: Optional[torch.Tensor] = None, soft_cap: float = 0.0,
+                 slopes: Optional[Sequence[float]] = None):
+        self.softmax_scale, self.window, self.n_sink, self.soft_cap = softmax_scale, window, n_sink, soft_cap
+        self.prefix_len = prefix_len
+        self.slopes = None if slopes is None else (ctypes.c_float * len(slopes))(*[float(x) for x in slopes])
+
+    def to_c(self, B: int, Hq: int) -> ScoreDescC:
+        _expect(self.prefix_len, (B,), torch.int32, "prefix_len")
+        if self.slopes is not None and len(self.slopes) != Hq:
+            raise ValueError(f"slopes must have one value for each of the {Hq} query heads, got {len(self.slopes)}")
+        c = ScoreDescC(self.softmax_scale, self.soft_cap, self.window, self.n_sink, _ptr(self.prefix_len))
+        if self.slopes is not None:
+            c.slopes = ctypes.cast(self.slopes, ctypes.POINTER(ctypes.c_float))
+        return c
+
+
+def _rows(t: torch.Tensor, what: str, H: Optional[int] = None, D: Optional[int] = None):
+    """(address, row stride in elements) of a CUDA tensor [T, H, D] whose heads lie
+    together; rows may be further apart (a slice of a fused projection)."""
+    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (D is not None and t.shape[2] != D):
+        raise ValueError(f"{what} must be [rows, {H or 'heads'}, {D or 'D'}], got shape {tuple(t.shape)}")
+    T, h, d = t.shape
+    sr, sh, sd = t.stride()
+    if T <= 1:
+        sr = h * d
+    if t.numel() > 0 and ((sd != 1 and d > 1) or (sh != d and h > 1)):
+        raise ValueError(f"the heads of a row of {what} must be contiguous, got strides {t.stride()}")
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be CUDA tensors, got one on {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device (cuda:{torch.cuda.current_device()}), "
+                         f"got one on {t.device}")
+    return t.data_ptr(), sr
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A new tensor that belongs to the stream the kernels run on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def token_rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: TokenRope, transpose: bool = False,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotate x [T, H, D] (bf16 or f32) at its tokens' positions (int32 [T]);
+    transpose=True applies the transposed rotation: the gradient. out may be x."""
+    xp, xs = _rows(x, "x")
+    T, H, D = x.shape
+    _expect(positions, (T,), torch.int32, "positions")
+    if out is None:
+        out = _empty(x.shape, x.dtype, x, stream)
+    elif out.dtype != x.dtype or out.shape != x.shape:
+        raise ValueError(f"out must be a {x.dtype} tensor of shape {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
+    op, os_ = _rows(out, "out")
+    if T == 0:
+        return out
+    _check(lib().ll_token_rope_apply(xp, xs, op, os_, _dtype_code(x.dtype), _ptr(positions), T, H, D, rope.to_c(),
+                                     int(transpose), _stream(stream)))
+    return out
+
+
+def _pool_c(cache: PagedKVCache) -> PagedCacheC:
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        _ptr(t)
+    return cache.to_c()
+
+
+def paged_append(cache: PagedKVCache, batch: TokenBatch, k: torch.Tensor, v: torch.Tensor,
+                 rope: Optional[TokenRope] = None, stream=None) -> None:
+    """Write the batch's new tokens, k and v [total_q, H, D] bf16, into their
+    pages, K rotated at its positions (ll_paged_append). Rows may be strided."""
+    kp, ks = _rows(k, "k", cache.H, cache.D)
+    vp, vs = _rows(v, "v", cache.H, cache.D)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have one shape and dtype")
+    if k.shape[0] == 0:
+        return
+    _check(lib().ll_paged_append(_pool_c(cache), batch.to_c(k.shape[0]), kp, ks, vp, vs, _dtype_code(k.dtype),
+                                 None if rope is None else rope.to_c(), _stream(stream)))
+
+
+def paged_attention_workspace_bytes(cache: PagedKVCache, batch: TokenBatch, total_q: int, Hq: int) -> int:
+    c = TokenBatchC(1 << 12, 1 << 12, 1 << 12, batch.B, batch.max_pages, total_q, batch.max_q, batch.max_kv)
+    return int(lib().ll_paged_attention_workspace_bytes(cache.to_c(), c, Hq))
+
+
+def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: TokenBatch, rope: Optional[TokenRope] = None,
+                    scores: Optional[Scores] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Attention of the batch's rows q [total_q, Hq, D] (bf16, rows may be
+    strided; rotated here when rope is given) over the pool, which already holds
+    their keys and values (ll_paged_attention). Rows of no sequence are not
+    written: they keep what `out` held."""
+    T, Hq = q.shape[0], q.shape[1]
+    qp, qs = _rows(q, "q", None, cache.D)
+    if out is None:
+        out = _empty((T, Hq, cache.D), q.dtype, q, stream)
+    _expect(out, (T, Hq, cache.D), q.dtype, "out")
+    _expect(lse, (T, Hq), torch.float32, "lse")
+    if T == 0:
+        return out
+    L, pool, tokens = lib(), _pool_c(cache), batch.to_c(T)
+    if workspace is None:
+        n = L.ll_paged_attention_workspace_bytes(pool, tokens, Hq)
+        if n:
+            workspace = _empty((n,), torch.uint8, q, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(L.ll_paged_attention(qp, qs, _dtype_code(q.dtype), Hq, pool, tokens, None if rope is None else rope.to_c(),
+                                None if scores is None else scores.to_c(batch.B, Hq), _ptr(out), _ptr(lse),
+                                _ptr(workspace), ws_bytes, _stream(stream)))
+    return out

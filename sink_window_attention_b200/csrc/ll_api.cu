@@ -983,3 +983,5 @@ ll_status ll_kv_recache(const ll_kvcache* cache, const void* x, int d_model, con
 }
 
 }  // extern "C"
+
+#include "ll_paged_api.cuh"

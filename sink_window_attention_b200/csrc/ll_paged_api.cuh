@@ -1,0 +1,383 @@
+// ll_paged_api.cuh — host side of the token-stream entry points (the last part
+// of ll_api.cu: uses its error, alignment and per-device helpers).
+#pragma once
+
+#include "ll_paged_attention.cuh"
+#include "ll_tokens.cuh"
+
+namespace {
+
+static_assert(LL_MAX_TOKEN_HEADS == ll::kMaxTokenHeads && LL_MAX_TOKEN_PAIRS == ll::kMaxTokenPairs, "header limits");
+
+ll_status make_token_rope(const ll_token_rope_desc* r, int D, int transpose, ll::TokenRope* out) {
+  std::memset(out, 0, sizeof(*out));
+  if (r == nullptr) return LL_OK;  // no rotation
+  if (r->rot_dim < 16 || r->rot_dim % 16 != 0 || r->rot_dim > 2 * LL_MAX_TOKEN_PAIRS || r->rot_dim > D)
+    return fail(LL_ERR_INVALID_ARG, "rot_dim = %d must be a multiple of 16 in [16, min(%d, D = %d)]", r->rot_dim,
+                2 * LL_MAX_TOKEN_PAIRS, D);
+  if (r->layout != LL_ROPE_INTERLEAVED && r->layout != LL_ROPE_HALF)
+    return fail(LL_ERR_INVALID_ARG, "unknown rope layout %d", r->layout);
+  if (!std::isfinite(r->amplitude)) return fail(LL_ERR_INVALID_ARG, "rope amplitude must be finite");
+  out->rot = r->rot_dim;
+  out->half = r->layout == LL_ROPE_HALF;
+  out->amp = r->amplitude;
+  out->sign = transpose ? -1.f : 1.f;
+  for (int i = 0; i < r->rot_dim / 2; ++i) out->turns[i] = r->turns[i];
+  return LL_OK;
+}
+
+ll_status check_paged_cache(const ll_paged_cache* c) {
+  if (c == nullptr) return fail(LL_ERR_INVALID_ARG, "cache is NULL");
+  if (c->k == nullptr || c->v == nullptr) return fail(LL_ERR_INVALID_ARG, "cache k/v pointer is NULL");
+  if (!aligned16(c->k) || !aligned16(c->v)) return fail(LL_ERR_INVALID_ARG, "cache k/v must be 16-byte aligned");
+  if (c->dtype != LL_BF16 && c->dtype != LL_FP8_E4M3)
+    return fail(LL_ERR_INVALID_ARG, "a paged cache is BF16 or FP8_E4M3 (got dtype %d)", (int)c->dtype);
+  if (c->dtype == LL_FP8_E4M3 && (c->k_scale == nullptr || c->v_scale == nullptr))
+    return fail(LL_ERR_INVALID_ARG, "an FP8 cache needs k_scale and v_scale");
+  if (c->dtype == LL_FP8_E4M3 && (!aligned4(c->k_scale) || !aligned4(c->v_scale)))
+    return fail(LL_ERR_INVALID_ARG, "k_scale and v_scale must be 4-byte aligned");
+  if (c->n_pages < 1 || c->H < 1) return fail(LL_ERR_INVALID_ARG, "cache sizes must be positive (n_pages=%d H=%d)",
+                                              c->n_pages, c->H);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return fail(LL_ERR_INVALID_ARG, "page_size = %d must be 16, 32, 64 or 128", c->page_size);
+  if (c->D != 64 && c->D != 128) return fail(LL_ERR_INVALID_ARG, "D = %d must be 64 or 128", c->D);
+  if (c->H > LL_MAX_TOKEN_HEADS) return fail(LL_ERR_INVALID_ARG, "H = %d exceeds %d", c->H, LL_MAX_TOKEN_HEADS);
+  return LL_OK;
+}
+
+ll_status check_batch(const ll_token_batch* t) {
+  if (t == nullptr) return fail(LL_ERR_INVALID_ARG, "batch is NULL");
+  if (t->q_start == nullptr || t->kv_len == nullptr || t->page_table == nullptr)
+    return fail(LL_ERR_INVALID_ARG, "q_start, kv_len and page_table must be non-NULL");
+  if (!aligned4(t->q_start) || !aligned4(t->kv_len) || !aligned4(t->page_table))
+    return fail(LL_ERR_INVALID_ARG, "q_start, kv_len and page_table must be 4-byte aligned");
+  if (t->B < 1 || t->max_pages < 1) return fail(LL_ERR_INVALID_ARG, "B = %d and max_pages = %d must be positive", t->B,
+                                                t->max_pages);
+  if (t->B > 65535) return fail(LL_ERR_INVALID_ARG, "B = %d exceeds 65535", t->B);
+  if (t->total_q < 0 || t->max_q < 0 || t->max_kv < 0)
+    return fail(LL_ERR_INVALID_ARG, "total_q, max_q and max_kv must be >= 0");
+  return LL_OK;
+}
+
+ll_status check_rows(const char* what, const void* x, long long stride, int H, int D) {
+  if (x == nullptr) return fail(LL_ERR_INVALID_ARG, "%s must be non-NULL", what);
+  if (!aligned16(x)) return fail(LL_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+  if (stride % 8 != 0 || stride < static_cast<long long>(H) * D)
+    return fail(LL_ERR_INVALID_ARG, "the row stride %lld of %s must be a multiple of 8 and at least H * D = %lld", stride,
+                what, static_cast<long long>(H) * D);
+  return LL_OK;
+}
+
+ll::TokenBatch to_batch(const ll_token_batch* t) {
+  ll::TokenBatch b;
+  b.q_start = t->q_start;
+  b.kv_len = t->kv_len;
+  b.page_table = t->page_table;
+  b.B = t->B;
+  b.max_pages = t->max_pages;
+  b.total_q = t->total_q;
+  b.max_q = t->max_q < t->total_q ? t->max_q : t->total_q;
+  b.max_kv = t->max_kv;
+  return b;
+}
+
+ll::PagedPool to_pool(const ll_paged_cache* c) {
+  ll::PagedPool p;
+  p.k = c->k;
+  p.v = c->v;
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.n_pages = c->n_pages;
+  p.page_size = c->page_size;
+  p.H = c->H;
+  p.D = c->D;
+  return p;
+}
+
+// Dynamic shared memory above the 48 KiB that a launch may use unasked.
+template <class K>
+ll_status allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
+  return once_per_device(done, [&]() -> ll_status {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return check_launch("cudaFuncSetAttribute");
+    return LL_OK;
+  });
+}
+
+// How a call's rows and keys are divided among blocks. A function of the host's
+// bounds alone, so the workspace size is known before the call.
+struct AttnPlan {
+  int row_tile, key_tile, row_tiles, chunk, nsplit;
+};
+
+AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq) {
+  AttnPlan a;
+  const int group = Hq / c->H;
+  const long long max_q = t->max_q < t->total_q ? t->max_q : t->total_q;
+  const long long cap = static_cast<long long>(t->max_pages) * c->page_size;
+  const long long max_kv = t->max_kv < cap ? t->max_kv : cap;
+  a.row_tile = 16;
+  a.key_tile = 16;
+  a.row_tiles = static_cast<int>((max_q * group + a.row_tile - 1) / a.row_tile);
+  // at most (window and prefix only shorten a range)
+  const long long nt = max_kv > 0 ? (max_kv + a.key_tile - 1) / a.key_tile : 1;
+  const long long units = static_cast<long long>(t->B) * c->H * a.row_tiles;
+  const long long slots = 3ll * num_sms();
+  long long chunk = units > 0 ? nt * units / (2 * slots) : nt;
+  if (chunk < 16) chunk = 16;
+  a.chunk = static_cast<int>(chunk < nt ? chunk : nt);
+  a.nsplit = static_cast<int>((nt + a.chunk - 1) / a.chunk);
+  return a;
+}
+
+size_t paged_workspace(const AttnPlan& a, const ll_token_batch* t, int Hq, int D) {
+  if (a.nsplit <= 1) return 0;
+  return align256(static_cast<size_t>(t->total_q) * Hq * a.nsplit * D * sizeof(float)) +
+         align256(static_cast<size_t>(t->total_q) * Hq * a.nsplit * sizeof(float2));
+}
+
+template <class TR>
+ll_status launch_paged_decode(const ll::PagedAttnParams& p, cudaStream_t s) {
+  auto kern = ll::paged_decode_kernel<TR>;
+  static std::atomic<unsigned long long> done{0};
+  ll_status st = allow_smem(kern, TR::SMEM, done);
+  if (st != LL_OK) return st;
+  kern<<<dim3(p.nsplit * p.row_tiles, p.pool.H, p.batch.B), TR::THREADS, TR::SMEM, s>>>(p);
+  return check_launch("paged_decode_kernel");
+}
+
+// The join starts while the pieces' kernel drains and waits for its end on the
+// device, which hides most of a launch.
+template <int D>
+ll_status launch_paged_join(const ll::PagedAttnParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  const long long warps = static_cast<long long>(p.batch.max_q) * p.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + ll::kJoinThreads / 32 - 1) / (ll::kJoinThreads / 32)), p.batch.B);
+  cfg.blockDim = dim3(ll::kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, ll::paged_join_kernel<D>, p);
+  return check_launch("paged_join_kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+ll_status ll_token_rope_init(ll_token_rope_desc* desc, int rot_dim, int layout, double theta0, double scale,
+                             double original_len, double beta_fast, double beta_slow, double amplitude) {
+  g_last_error.clear();
+  if (desc == nullptr) return fail(LL_ERR_INVALID_ARG, "desc is NULL");
+  if (rot_dim < 16 || rot_dim % 16 != 0 || rot_dim > 2 * LL_MAX_TOKEN_PAIRS)
+    return fail(LL_ERR_INVALID_ARG, "rot_dim = %d must be a multiple of 16 in [16, %d]", rot_dim, 2 * LL_MAX_TOKEN_PAIRS);
+  if (layout != LL_ROPE_INTERLEAVED && layout != LL_ROPE_HALF)
+    return fail(LL_ERR_INVALID_ARG, "unknown rope layout %d", layout);
+  if (!(theta0 > 1.0) || !std::isfinite(theta0))
+    return fail(LL_ERR_INVALID_ARG, "rope theta0 must be a finite value > 1");
+  if (!(scale > 0.0 && scale <= 1.0)) return fail(LL_ERR_INVALID_ARG, "rope scale must lie in (0, 1]");
+  if (!(original_len >= 0.0) || !std::isfinite(original_len))
+    return fail(LL_ERR_INVALID_ARG, "rope original_len must be a finite value >= 0");
+  if (original_len > 0.0 && !(beta_slow >= 0.0 && beta_fast > beta_slow && std::isfinite(beta_fast)))
+    return fail(LL_ERR_INVALID_ARG, "need 0 <= beta_slow < beta_fast, finite");
+  if (!std::isfinite(amplitude) || !std::isfinite(static_cast<float>(amplitude)))
+    return fail(LL_ERR_INVALID_ARG, "rope amplitude must be finite");
+  std::memset(desc, 0, sizeof(*desc));
+  desc->rot_dim = rot_dim;
+  desc->layout = layout;
+  desc->amplitude = static_cast<float>(amplitude);
+  constexpr double kTwoPi = 6.283185307179586476925;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double w = std::pow(theta0, -2.0 * i / rot_dim);
+    double keep = 0.0;
+    if (original_len > 0.0) {
+      keep = (original_len * w / kTwoPi - beta_slow) / (beta_fast - beta_slow);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+    }
+    // w <= 1, so the turn per position is below 1/6; the double's 53 bits put the
+    // angle of position 2^31 within 2^-24 of a turn
+    desc->turns[i] = static_cast<uint64_t>(std::ldexp(w * (keep + (1.0 - keep) * scale) / kTwoPi, 64));
+  }
+  return LL_OK;
+}
+
+ll_status ll_token_rope_apply(const void* x, long long x_stride, void* out, long long out_stride, ll_dtype dtype,
+                              const int32_t* positions, int T, int H, int D, const ll_token_rope_desc* rope,
+                              int transpose, void* stream) {
+  g_last_error.clear();
+  if (dtype != LL_F32 && dtype != LL_BF16) return fail(LL_ERR_INVALID_ARG, "dtype must be F32 or BF16");
+  if (rope == nullptr || positions == nullptr) return fail(LL_ERR_INVALID_ARG, "rope and positions must be non-NULL");
+  if (!aligned4(positions)) return fail(LL_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  if (T < 0 || H < 1 || D < 16 || D % 16 != 0)
+    return fail(LL_ERR_INVALID_ARG, "need T >= 0, H >= 1 and D a multiple of 16 (T=%d H=%d D=%d)", T, H, D);
+  if (D > 1024 || static_cast<long long>(H) * D >= (1ll << 24))
+    return fail(LL_ERR_UNSUPPORTED, "D = %d exceeds 1024 or H * D reaches 2^24", D);
+  ll_status st = check_rows("x", x, x_stride, H, D);
+  if (st != LL_OK) return st;
+  if ((st = check_rows("out", out, out_stride, H, D)) != LL_OK) return st;
+  ll::TokenRopeParams p;
+  if ((st = make_token_rope(rope, D, transpose, &p.rope)) != LL_OK) return st;
+  if (T == 0) return LL_OK;
+  p.x = x;
+  p.out = out;
+  p.x_stride = x_stride;
+  p.out_stride = out_stride;
+  p.positions = positions;
+  p.T = T;
+  p.H = H;
+  p.D = D;
+  // one token per block while that leaves SMs idle; from there on up to 8 tokens,
+  // and no more than three units per thread
+  const int per_token = H * (D / 16);
+  int tokens = 3 * ll::kTokenRopeThreads / per_token;
+  const int fill = T / (4 * num_sms());
+  tokens = tokens < fill ? tokens : fill;
+  p.tokens = tokens < 1 ? 1 : (tokens > 8 ? 8 : tokens);
+  const int grid = (T - 1) / p.tokens + 1;
+  const size_t smem = static_cast<size_t>(p.tokens) * (p.rope.rot / 2) * sizeof(float2);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == LL_F32)
+    ll::token_rope_kernel<float><<<grid, ll::kTokenRopeThreads, smem, s>>>(p);
+  else
+    ll::token_rope_kernel<__nv_bfloat16><<<grid, ll::kTokenRopeThreads, smem, s>>>(p);
+  return check_launch("token_rope_kernel");
+}
+
+ll_status ll_paged_append(const ll_paged_cache* cache, const ll_token_batch* batch, const void* k, long long k_stride,
+                          const void* v, long long v_stride, ll_dtype in_dtype, const ll_token_rope_desc* rope,
+                          void* stream) {
+  g_last_error.clear();
+  ll_status st = check_paged_cache(cache);
+  if (st != LL_OK) return st;
+  if ((st = check_batch(batch)) != LL_OK) return st;
+  if (in_dtype != LL_BF16) return fail(LL_ERR_INVALID_ARG, "k and v must be BF16");
+  if ((st = check_rows("k", k, k_stride, cache->H, cache->D)) != LL_OK) return st;
+  if ((st = check_rows("v", v, v_stride, cache->H, cache->D)) != LL_OK) return st;
+  ll::PagedAppendParams p{};
+  if ((st = make_token_rope(rope, cache->D, 0, &p.rope)) != LL_OK) return st;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.pool = to_pool(cache);
+  p.batch = to_batch(batch);
+  const int max_q = p.batch.max_q;
+  if (max_q == 0) return LL_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int pairs = p.rope.rot / 2, ps = cache->page_size;
+  if (cache->dtype == LL_BF16) {
+    const int per_token = cache->H * (cache->D / 16);
+    int tokens = 2 * ll::kPagedAppendThreads / per_token;
+    const long long fill = static_cast<long long>(max_q) * batch->B / (4 * num_sms());
+    if (tokens > fill) tokens = static_cast<int>(fill);
+    p.tokens = tokens < 1 ? 1 : (tokens > 16 ? 16 : tokens);
+    ll::paged_append_bf16_kernel<<<dim3((max_q - 1) / p.tokens + 1, batch->B), ll::kPagedAppendThreads,
+                                   static_cast<size_t>(p.tokens) * pairs * sizeof(float2), s>>>(p);
+    return check_launch("paged_append_bf16_kernel");
+  }
+  const int units = ps * (cache->D / 16);  // 16-element units of a page and head
+  p.head_threads = units < ll::kPagedAppendThreads ? units : ll::kPagedAppendThreads;
+  p.heads = ll::kPagedAppendThreads / p.head_threads;
+  // pages that max_q tokens can touch, wherever the first of them stands
+  const int touched = (max_q - 1) / ps + ((max_q - 1) % ps != 0 ? 2 : 1);
+  const dim3 grid(touched, batch->B, (cache->H + p.heads - 1) / p.heads);
+  const size_t smem = static_cast<size_t>(max_q < ps ? max_q : ps) * pairs * sizeof(float2);
+  auto launch = [&](auto kern, std::atomic<unsigned long long>& done) -> ll_status {
+    const ll_status a = allow_smem(kern, 128 * LL_MAX_TOKEN_PAIRS * static_cast<int>(sizeof(float2)), done);
+    if (a != LL_OK) return a;
+    kern<<<grid, ll::kPagedAppendThreads, smem, s>>>(p);
+    return check_launch("paged_append_e4m3_kernel");
+  };
+  static std::atomic<unsigned long long> done[3];
+  switch (units / p.head_threads) {
+    case 1: return launch(ll::paged_append_e4m3_kernel<1>, done[0]);
+    case 2: return launch(ll::paged_append_e4m3_kernel<2>, done[1]);
+    default: return launch(ll::paged_append_e4m3_kernel<4>, done[2]);
+  }
+}
+
+size_t ll_paged_attention_workspace_bytes(const ll_paged_cache* cache, const ll_token_batch* batch, int Hq) {
+  if (check_paged_cache(cache) != LL_OK || check_batch(batch) != LL_OK || Hq < 1 || Hq % cache->H != 0 ||
+      Hq > LL_MAX_TOKEN_HEADS)
+    return 0;
+  return paged_workspace(plan_attention(cache, batch, Hq), batch, Hq, cache->D);
+}
+
+ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype, int Hq, const ll_paged_cache* cache,
+                             const ll_token_batch* batch, const ll_token_rope_desc* rope, const ll_score_desc* scores,
+                             void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  ll_status st = check_paged_cache(cache);
+  if (st != LL_OK) return st;
+  if ((st = check_batch(batch)) != LL_OK) return st;
+  if (q_dtype != LL_BF16) return fail(LL_ERR_INVALID_ARG, "q must be BF16");
+  if (Hq < 1 || Hq % cache->H != 0)
+    return fail(LL_ERR_INVALID_ARG, "Hq = %d must be a positive multiple of the cache's H = %d", Hq, cache->H);
+  if (Hq > LL_MAX_TOKEN_HEADS) return fail(LL_ERR_UNSUPPORTED, "Hq = %d exceeds %d", Hq, LL_MAX_TOKEN_HEADS);
+  if ((st = check_rows("q", q, q_stride, Hq, cache->D)) != LL_OK) return st;
+  if (out == nullptr || !aligned16(out)) return fail(LL_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
+  if (!aligned4(lse)) return fail(LL_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  ll::PagedAttnParams p{};
+  if ((st = make_token_rope(rope, cache->D, 0, &p.rope)) != LL_OK) return st;
+  const ll_score_desc plain = {};
+  const ll_score_desc* sc = scores ? scores : &plain;
+  if (!(sc->softmax_scale >= 0.f) || !std::isfinite(sc->softmax_scale))
+    return fail(LL_ERR_INVALID_ARG, "softmax_scale must be finite and >= 0");
+  if (!(sc->soft_cap >= 0.f) || !std::isfinite(sc->soft_cap))
+    return fail(LL_ERR_INVALID_ARG, "soft_cap must be finite and >= 0");
+  if (sc->window < 0 || sc->n_sink < 0) return fail(LL_ERR_INVALID_ARG, "window and n_sink must be >= 0");
+  if (!aligned4(sc->prefix_len)) return fail(LL_ERR_INVALID_ARG, "prefix_len must be 4-byte aligned");
+  const float scale = sc->softmax_scale > 0.f ? sc->softmax_scale : 1.0f / std::sqrt(static_cast<float>(cache->D));
+  p.sc.pre = sc->soft_cap > 0.f ? scale / sc->soft_cap : scale * ll::kLog2e;
+  p.sc.cap2 = sc->soft_cap * ll::kLog2e;
+  p.sc.window = sc->window;
+  p.sc.n_sink = sc->n_sink;
+  p.sc.prefix_len = sc->prefix_len;
+  if (sc->slopes != nullptr) {
+    p.sc.biased = 1;
+    for (int h = 0; h < Hq; ++h) {
+      if (!std::isfinite(sc->slopes[h])) return fail(LL_ERR_INVALID_ARG, "slopes[%d] is not finite", h);
+      p.sc.slope2[h] = sc->slopes[h] * ll::kLog2e;
+    }
+  }
+  const AttnPlan plan = plan_attention(cache, batch, Hq);
+  const size_t need = paged_workspace(plan, batch, Hq, cache->D);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return fail(LL_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
+  if (need > 0 && !aligned16(workspace)) return fail(LL_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.Hq = Hq;
+  p.group = Hq / cache->H;
+  p.pool = to_pool(cache);
+  p.batch = to_batch(batch);
+  p.row_tile = plan.row_tile;
+  p.key_tile = plan.key_tile;
+  p.row_tiles = plan.row_tiles;
+  p.chunk = plan.chunk;
+  p.nsplit = plan.nsplit;
+  if (need > 0) {
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(
+        static_cast<char*>(workspace) +
+        align256(static_cast<size_t>(batch->total_q) * Hq * plan.nsplit * cache->D * sizeof(float)));
+  }
+  if (p.batch.max_q == 0) return LL_OK;
+  if (static_cast<long long>(p.nsplit) * p.row_tiles > INT_MAX)
+    return fail(LL_ERR_UNSUPPORTED, "the call needs more than 2^31 - 1 blocks");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->dtype == LL_FP8_E4M3;
+  if (cache->D == 128)
+    st = e4m3 ? launch_paged_decode<ll::DecodeTraits<128, true>>(p, s) : launch_paged_decode<ll::DecodeTraits<128, false>>(p, s);
+  else
+    st = e4m3 ? launch_paged_decode<ll::DecodeTraits<64, true>>(p, s) : launch_paged_decode<ll::DecodeTraits<64, false>>(p, s);
+  if (st != LL_OK || p.nsplit == 1) return st;
+  return cache->D == 128 ? launch_paged_join<128>(p, s) : launch_paged_join<64>(p, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,623 @@
+// ll_paged_attention.cuh — attention of a ragged batch of token rows over a
+// paged pool: the kernel for few rows (decode), and the one that joins the
+// pieces of a split key range.
+//
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(x_j - m),
+//   x = scale q.k, soft-capped, biased by distance; masked keys have no x.
+#pragma once
+
+#include "ll_tokens.cuh"
+
+namespace ll {
+
+constexpr int kMaxTokenHeads = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct ScoreParams {
+  float pre;     // factor on q.k: softmax_scale * (cap > 0 ? 1 / cap : log2 e)
+  float cap2;    // cap * log2 e, or 0
+  int window, n_sink;
+  const int* prefix_len;
+  int biased;
+  float slope2[kMaxTokenHeads];  // slope * log2 e
+};
+
+struct PagedAttnParams {
+  const __nv_bfloat16* q;
+  long long q_stride;
+  __nv_bfloat16* out;
+  float* lse;
+  int Hq, group;     // query heads, and how many share a K/V head
+  PagedPool pool;
+  TokenBatch batch;
+  TokenRope rope;
+  ScoreParams sc;
+  int row_tile;      // rows (token, query head of the group) of a unit
+  int key_tile;      // keys per step; pieces begin at multiples of it
+  int chunk;         // key tiles per piece
+  int nsplit;        // pieces at most
+  int row_tiles;     // units of a sequence and K/V head at most
+  float* part_o;     // [total_q][Hq][nsplit][D], unnormalised
+  float2* part_ml;   // [total_q][Hq][nsplit]: (max, sum), max in log2 units
+};
+
+// The keys that some row of a unit sees, as two runs of key tiles: [0, a_end)
+// (prefix and sinks) and [w_beg, w_end) (window). Rows of the unit stand at
+// positions p_lo .. p_hi.
+struct KeyRange {
+  int prefix, always, lo, upper;  // keys [0, always) and [lo, upper) are seen by some row
+  int a_end, w_beg, nt;           // tiles in all
+  __device__ __forceinline__ int tile(int i) const { return i < a_end ? i : i - a_end + w_beg; }
+  __device__ __forceinline__ bool some_row_sees(int j) const { return j < always || (j >= lo && j < upper); }
+};
+
+__device__ __forceinline__ KeyRange key_range(const ScoreParams& sc, int b, const SeqView& s, long long p_lo,
+                                              long long p_hi, int key_tile) {
+  KeyRange r;
+  int prefix = sc.prefix_len ? sc.prefix_len[b] : 0;
+  r.prefix = prefix < 0 ? 0 : (prefix < s.len ? prefix : s.len);
+  const long long causal = p_hi + 1 < s.len ? p_hi + 1 : s.len;  // keys [0, causal) stand at or before the last row
+  r.upper = static_cast<int>(causal > 0 ? causal : 0);
+  const long long lo = sc.window > 0 ? p_lo - sc.window + 1 : 0;
+  r.lo = static_cast<int>(lo < 0 ? 0 : (lo < r.upper ? lo : r.upper));
+  const int sink = sc.window > 0 ? (sc.n_sink < r.upper ? sc.n_sink : r.upper) : 0;
+  r.always = sink > r.prefix ? sink : r.prefix;
+  r.a_end = (r.always + key_tile - 1) / key_tile;
+  const int wb = r.lo / key_tile;
+  r.w_beg = wb > r.a_end ? wb : r.a_end;
+  const int w_end = (r.upper + key_tile - 1) / key_tile;
+  r.nt = r.a_end + (w_end > r.w_beg ? w_end - r.w_beg : 0);
+  return r;
+}
+
+__device__ __forceinline__ bool row_sees(const ScoreParams& sc, const KeyRange& r, int len, long long p, int j) {
+  if (j < r.prefix) return true;
+  return j <= p && j < len && (sc.window == 0 || p - j < sc.window || j < sc.n_sink);
+}
+
+// Positions of a unit's first and last row.
+__device__ __forceinline__ void unit_positions(const PagedAttnParams& p, const SeqView& s, int r0, long long& lo,
+                                               long long& hi) {
+  const int last = min(r0 + p.row_tile, s.nq * p.group) - 1;
+  lo = s.first_pos + r0 / p.group;
+  hi = s.first_pos + last / p.group;
+}
+
+__device__ __forceinline__ int piece_count(const PagedAttnParams& p, int nt) {
+  const int n = (nt + p.chunk - 1) / p.chunk;
+  return n > 1 ? n : 1;
+}
+
+// tanh(y) = 1 - 2 / (1 + e^2y): within about 2e-7 absolute, which the cap scales
+// to some 1e-5 of a score (the hardware's own tanh is off by 5e-4).
+__device__ __forceinline__ float tanh_accurate(float y) {
+  return 1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * y));
+}
+
+// The score in log2 units from s = q.k.
+__device__ __forceinline__ float score2(const ScoreParams& sc, float s, float factor) {
+  const float y = s * factor;
+  return sc.cap2 > 0.f ? sc.cap2 * tanh_accurate(y) : y;
+}
+
+// The power of two 2^e with 2^e <= a < 2^(e+1), kept within [2^-125, 2^126] (1 for 0).
+__device__ __forceinline__ float power_below(float a) {
+  const int e = static_cast<int>(__float_as_uint(a) >> 23);
+  if (e == 0) return 1.f;
+  return __uint_as_float(static_cast<uint32_t>(e < 2 ? 2 : (e > 253 ? 253 : e)) << 23);
+}
+
+// floor(log2(s)) of a scale, kept within [-60, 60] (a zero scale: -60): only a
+// reference for exponents, which cancels. The bounds keep p in fp32.
+__device__ __forceinline__ float scale_exponent(float s) {
+  const int e = static_cast<int>(__float_as_uint(s) >> 23 & 255u) - 127;
+  return static_cast<float>(e < -60 ? -60 : (e > 60 ? 60 : e));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ---------------------------------------------------------------------------
+// cp.async and mma.sync
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8)
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 codes as two halves (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (decode). One block: 16 rows of a sequence and K/V head against a
+// piece of its keys; the block's warps take 16-key tiles in turn, each with a
+// ring of its own in shared memory that cp.async keeps full, and meet once at
+// the end. What bounds it is the pool's bytes, so nothing but loads in flight
+// matters: 4 warps x (STAGES - 1) tiles of K and V per block, several blocks
+// per SM. The matrix instruction is the warp-level one (16 x 8 x 16): a
+// tensor-memory tile has 128 rows, of which a decode step fills 1 to 16.
+//
+// The reduction index of an MMA may be permuted when both operands are, so
+// neither K nor V needs a transposing load:
+//  * S = Q K^T: lane (g, t) holds key g and takes whole 16-byte chunks t, t + 4,
+//    .. of its row; Q's fragments use the same order of d.
+//  * O = P V: the lane's columns of S are keys 2t, 2t+1, 2t+8, 2t+9, so P is an
+//    A operand as it stands; the lane reads those four rows of V at chunk g
+//    (+ 8), and byte permutes pair two keys at the same d.
+// ---------------------------------------------------------------------------
+template <int D_, bool E4M3_>
+struct DecodeTraits {
+  static constexpr int D = D_;
+  static constexpr bool E4M3 = E4M3_;
+  static constexpr int ES = E4M3 ? 1 : 2;
+  static constexpr int ROWB = D * ES;
+  static constexpr int CH = ROWB / 16;      // chunks per row
+  static constexpr int KC = CH / 4;         // chunks of K per lane
+  static constexpr int EPC = 16 / ES;       // elements per chunk
+  static constexpr int KS = D / 16;         // MMAs over d
+  static constexpr int NT = D / 8;          // MMAs over O's columns
+  static constexpr int TILE = 16 * ROWB;
+  static constexpr int NW = 4;
+  static constexpr int THREADS = NW * 32;
+  static constexpr int STAGES = ROWB >= 256 ? 3 : 4;
+  static constexpr int RING = NW * STAGES * 2 * TILE;
+  static constexpr int QP = D + 8;          // 16-bit elements between rows of Q
+  static constexpr int BLOCKS = ROWB >= 256 ? 2 : 3;  // per SM, by shared memory
+  static constexpr int META = NW * STAGES * 16;
+  static constexpr int SMEM = RING + META + 16 * QP * 2 + 16 * 4 + 2 * NW * 16 * 4;
+  static_assert(NW * 16 * D * 4 <= RING, "the warps' O must fit the ring");
+};
+
+template <int CH>
+__device__ __forceinline__ int swz(int row, int c) {
+  if constexpr (CH == 4) return c ^ ((row >> 1) & 3);
+  return c ^ ((((row ^ (row >> 2)) & 1) << 2) | (row & 2));
+}
+
+template <class TR>
+__global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(const PagedAttnParams p) {
+  constexpr int D = TR::D, CH = TR::CH, NW = TR::NW, STAGES = TR::STAGES, TILE = TR::TILE;
+  constexpr bool E4M3 = TR::E4M3;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* s_ring = smem;
+  float* s_meta = reinterpret_cast<float*>(smem + TR::RING);  // [NW][STAGES][4]: K scale, V scale, page mapped
+  uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + TR::RING + TR::META);  // [16][QP]
+  float* s_qf = reinterpret_cast<float*>(s_q + 16 * TR::QP);                // [16]
+  float* s_m = s_qf + 16;                                                   // [NW][16]
+  float* s_l = s_m + NW * 16;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int rt = blockIdx.x % p.row_tiles, split = blockIdx.x / p.row_tiles;
+  const int hkv = blockIdx.y, b = blockIdx.z;
+  const int ps = p.pool.page_size;
+  const SeqView s = seq_view(p.batch, b, ps);
+  const int rows = s.nq * p.group, r0 = rt * 16;
+  if (r0 >= rows) return;
+  long long p_lo, p_hi;
+  unit_positions(p, s, r0, p_lo, p_hi);
+  const KeyRange kr = key_range(p.sc, b, s, p_lo, p_hi, 16);
+  const int pieces = piece_count(p, kr.nt);
+  if (split >= pieces) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t_beg = split * p.chunk + warp;
+  const int t_end = min(kr.nt, (split + 1) * p.chunk);
+  const int n_my = t_end > t_beg ? (t_end - t_beg + NW - 1) / NW : 0;
+
+  // ---- the ring
+  const uint32_t ring = smem_addr(s_ring) + warp * (STAGES * 2 * TILE);
+  const uint32_t meta = smem_addr(s_meta) + warp * (STAGES * 16);
+  const uint8_t* kp = static_cast<const uint8_t*>(p.pool.k);
+  const uint8_t* vp = static_cast<const uint8_t*>(p.pool.v);
+  int my_page = -1;
+  auto issue = [&](int k) {
+    if (k < n_my) {
+      if ((k & 31) == 0) {  // the pages of this warp's next 32 tiles, one per lane
+        const int kk = k + lane;
+        my_page = kk < n_my ? page_of(p.batch, b, kr.tile(t_beg + kk * NW) * 16 / ps, p.pool.n_pages) : -1;
+      }
+      const int page = __shfl_sync(0xffffffffu, my_page, k & 31);
+      const int key0 = kr.tile(t_beg + k * NW) * 16;
+      const int st = k % STAGES;
+      const size_t head = static_cast<size_t>(page < 0 ? 0 : page) * p.pool.H + hkv;
+      const size_t src = (head * ps + (key0 & (ps - 1))) * TR::ROWB;
+      const uint32_t dst = ring + st * (2 * TILE);
+#pragma unroll
+      for (int i = 0; i < TILE / 512; ++i) {
+        const int c = lane + 32 * i, row = c / CH, ch = c % CH;
+        const bool ok = page >= 0 && kr.some_row_sees(key0 + row);
+        const uint32_t to = dst + row * TR::ROWB + (swz<CH>(row, ch) << 4);
+        cp_async16(to, kp + src + c * 16, ok);
+        cp_async16(to + TILE, vp + src + c * 16, ok);
+      }
+      if constexpr (E4M3) {
+        if (lane < 2) cp_async4(meta + st * 16 + lane * 4, (lane ? p.pool.v_scale : p.pool.k_scale) + head, page >= 0);
+      }
+      if (lane == 2) s_meta[(warp * STAGES + st) * 4 + 2] = page >= 0 ? 1.f : 0.f;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < STAGES - 1; ++k) issue(k);
+
+  // ---- Q: rotated in fp32, rounded to the MMA's type
+  for (int i = threadIdx.x; i < 16 * (D / 16); i += TR::THREADS) {
+    const int r = i / (D / 16), c = i % (D / 16);
+    const int row = r0 + r, tok = row / p.group, h = hkv * p.group + row % p.group;
+    int lo, hi;
+    item_chunks(p.rope, c, lo, hi);
+    float x[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+    if (row < rows) {
+      const __nv_bfloat16* src = p.q + (s.q0 + tok) * p.q_stride + h * D;
+      load_chunk8<__nv_bfloat16>(src + lo * 8, x);
+      load_chunk8<__nv_bfloat16>(src + hi * 8, y);
+      if (c < (p.rope.rot >> 4)) {
+        float2 cs[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cs[e] = turn_of(p.rope, s.first_pos + tok, c * 8 + e);
+        rotate_item(p.rope, x, y, cs);
+      }
+    }
+    uint32_t w[8];
+    if constexpr (E4M3) {
+      // fp16 has bf16's precision and three bits more, but a short range: the
+      // row is divided by the power of two below its largest element
+      float a = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = fmax3(a, fabsf(x[e]), fabsf(y[e]));
+#pragma unroll
+      for (int o = D / 32; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      const float f = power_below(a), inv = 1.f / f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = pack_f16(x[2 * e] * inv, x[2 * e + 1] * inv);
+        w[4 + e] = pack_f16(y[2 * e] * inv, y[2 * e + 1] * inv);
+      }
+      if (c == 0) s_qf[r] = f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+        w[4 + e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+      }
+      if (c == 0) s_qf[r] = 1.f;
+    }
+    *reinterpret_cast<uint4*>(s_q + r * TR::QP + lo * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(s_q + r * TR::QP + hi * 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  __syncthreads();
+
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t aq[TR::KS][4];
+#pragma unroll
+  for (int j = 0; j < TR::KS; ++j) {
+    constexpr int U = TR::EPC / 4;  // MMAs per chunk
+    const int d = (t + 4 * (j / U)) * TR::EPC + 4 * (j % U);
+    const uint2 u0 = *reinterpret_cast<const uint2*>(s_q + g * TR::QP + d);
+    const uint2 u1 = *reinterpret_cast<const uint2*>(s_q + (g + 8) * TR::QP + d);
+    aq[j][0] = u0.x;
+    aq[j][1] = u1.x;
+    aq[j][2] = u0.y;
+    aq[j][3] = u1.y;
+  }
+  const float fac[2] = {s_qf[g] * p.sc.pre, s_qf[g + 8] * p.sc.pre};
+  const int prow[2] = {r0 + g, r0 + g + 8};
+  const long long pos[2] = {s.first_pos + prow[0] / p.group, s.first_pos + prow[1] / p.group};
+  float slope[2] = {0.f, 0.f};
+  if (p.sc.biased) {
+    slope[0] = p.sc.slope2[hkv * p.group + prow[0] % p.group];
+    slope[1] = p.sc.slope2[hkv * p.group + prow[1] % p.group];
+  }
+
+  float o[TR::NT][4];
+#pragma unroll
+  for (int n = 0; n < TR::NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+  // m: reference of the row's exponents (a running max, raised only when it is
+  // exceeded by 2^8: sums and O are rescaled rarely); l: this lane's share of the
+  // sum. Over an 8-bit pool V's codes enter the MMA as they are and their scale
+  // goes with P = p vs, so the reference is the max of x + log2(vs): P then stays
+  // inside fp16 whatever the pages' scales are, p itself is fp32.
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  for (int k = 0; k < n_my; ++k) {
+    cp_async_wait<STAGES - 2>();
+    __syncwarp();
+    const int st = k % STAGES;
+    const uint8_t* sk = s_ring + warp * (STAGES * 2 * TILE) + st * (2 * TILE);
+    const uint8_t* sv = sk + TILE;
+    const float4 mt = *reinterpret_cast<const float4*>(s_meta + (warp * STAGES + st) * 4);
+    const int key0 = kr.tile(t_beg + k * NW) * 16;
+    float sx[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sx[n][e] = 0.f;
+      const int row = g + 8 * n;
+#pragma unroll
+      for (int i = 0; i < TR::KC; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4*>(sk + row * TR::ROWB + (swz<CH>(row, t + 4 * i) << 4));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma16816<true>(sx[n], aq[i * 4 + e], e4m3x2_f16(w[e]), e4m3x2_f16(w[e] >> 16));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma16816<false>(sx[n], aq[i * 2 + e], w[2 * e], w[2 * e + 1]);
+        }
+      }
+    }
+    // scores in log2 units: x[row][key], keys 2t, 2t+1, 2t+8, 2t+9 of the tile
+    float x[2][4];
+    const float ks = E4M3 ? mt.x : 1.f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[r][e] = score2(p.sc, sx[e >> 1][2 * r + (e & 1)], fac[r] * ks);
+    if (p.sc.biased) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = key0 + 2 * t + (e & 1) + 8 * (e >> 1);
+          x[r][e] -= slope[r] * fabsf(static_cast<float>(pos[r] - j));
+        }
+    }
+    const bool all_seen = mt.z != 0.f && (key0 + 16 <= kr.prefix ||
+                                          (key0 + 15 <= p_lo && key0 + 16 <= s.len &&
+                                           (p.sc.window == 0 || p_hi - key0 < p.sc.window)));
+    if (!all_seen) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = key0 + 2 * t + (e & 1) + 8 * (e >> 1);
+          if (mt.z == 0.f || !row_sees(p.sc, kr, s.len, pos[r], j)) x[r][e] = -INFINITY;
+        }
+    }
+    const float vs = E4M3 ? mt.y : 1.f, c2 = E4M3 ? scale_exponent(vs) : 0.f;
+    float mx[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) mx[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])) + c2;
+    if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+      float al[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        const float nm = fmaxf(m[r], mx[r]);
+        al[r] = nm == -INFINITY ? 1.f : ex2(m[r] - nm);
+        m[r] = nm;
+        l[r] *= al[r];
+      }
+#pragma unroll
+      for (int n = 0; n < TR::NT; ++n) {
+        o[n][0] *= al[0];
+        o[n][1] *= al[0];
+        o[n][2] *= al[1];
+        o[n][3] *= al[1];
+      }
+    }
+    uint32_t pa[4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float ms = m[r] == -INFINITY ? 0.f : m[r];
+      float e0 = ex2(x[r][0] - ms), e1 = ex2(x[r][1] - ms), e2 = ex2(x[r][2] - ms), e3 = ex2(x[r][3] - ms);
+      l[r] += (e0 + e1) + (e2 + e3);
+      if constexpr (E4M3) {
+        pa[r] = pack_f16(e0 * vs, e1 * vs);
+        pa[2 + r] = pack_f16(e2 * vs, e3 * vs);
+      } else {
+        pa[r] = pack_bf16(e0, e1);
+        pa[2 + r] = pack_bf16(e2, e3);
+      }
+    }
+    // O += P V
+    if constexpr (E4M3 && CH == 4) {  // D = 64: half a chunk per lane
+      uint32_t w[4][2];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = 2 * t + (q & 1) + 8 * (q >> 1);
+        const uint2 u = *reinterpret_cast<const uint2*>(sv + row * TR::ROWB + (swz<CH>(row, g >> 1) << 4) + (g & 1) * 8);
+        w[q][0] = u.x;
+        w[q][1] = u.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t a01 = __byte_perm(w[0][i], w[1][i], 0x5140), a23 = __byte_perm(w[0][i], w[1][i], 0x7362);
+        const uint32_t c01 = __byte_perm(w[2][i], w[3][i], 0x5140), c23 = __byte_perm(w[2][i], w[3][i], 0x7362);
+        mma16816<true>(o[4 * i], pa, e4m3x2_f16(a01), e4m3x2_f16(c01));
+        mma16816<true>(o[4 * i + 1], pa, e4m3x2_f16(a01 >> 16), e4m3x2_f16(c01 >> 16));
+        mma16816<true>(o[4 * i + 2], pa, e4m3x2_f16(a23), e4m3x2_f16(c23));
+        mma16816<true>(o[4 * i + 3], pa, e4m3x2_f16(a23 >> 16), e4m3x2_f16(c23 >> 16));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH / 8; ++i) {
+        uint32_t w[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = 2 * t + (q & 1) + 8 * (q >> 1);
+          const uint4 u = *reinterpret_cast<const uint4*>(sv + row * TR::ROWB + (swz<CH>(row, g + 8 * i) << 4));
+          w[q][0] = u.x;
+          w[q][1] = u.y;
+          w[q][2] = u.z;
+          w[q][3] = u.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (E4M3) {
+            const uint32_t a01 = __byte_perm(w[0][e], w[1][e], 0x5140), a23 = __byte_perm(w[0][e], w[1][e], 0x7362);
+            const uint32_t c01 = __byte_perm(w[2][e], w[3][e], 0x5140), c23 = __byte_perm(w[2][e], w[3][e], 0x7362);
+            mma16816<true>(o[4 * e], pa, e4m3x2_f16(a01), e4m3x2_f16(c01));
+            mma16816<true>(o[4 * e + 1], pa, e4m3x2_f16(a01 >> 16), e4m3x2_f16(c01 >> 16));
+            mma16816<true>(o[4 * e + 2], pa, e4m3x2_f16(a23), e4m3x2_f16(c23));
+            mma16816<true>(o[4 * e + 3], pa, e4m3x2_f16(a23 >> 16), e4m3x2_f16(c23 >> 16));
+          } else {
+            mma16816<false>(o[i * 8 + 2 * e], pa, __byte_perm(w[0][e], w[1][e], 0x5410),
+                            __byte_perm(w[2][e], w[3][e], 0x5410));
+            mma16816<false>(o[i * 8 + 2 * e + 1], pa, __byte_perm(w[0][e], w[1][e], 0x7632),
+                            __byte_perm(w[2][e], w[3][e], 0x7632));
+          }
+        }
+      }
+    }
+    __syncwarp();  // every lane is done with the stage
+    issue(k + STAGES - 1);
+  }
+
+  // ---- join the block's warps
+  cp_async_wait<0>();
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  }
+  if (t == 0) {
+    s_m[warp * 16 + g] = m[0];
+    s_m[warp * 16 + g + 8] = m[1];
+    s_l[warp * 16 + g] = l[0];
+    s_l[warp * 16 + g + 8] = l[1];
+  }
+  __syncthreads();
+  float* s_o = reinterpret_cast<float*>(s_ring);  // [NW][16][D]
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + g + 8 * r]);
+    const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - M);
+    float* dst = s_o + (warp * 16 + g + 8 * r) * D;
+#pragma unroll
+    for (int n = 0; n < TR::NT; ++n) {
+      // column c (0..7) of MMA n is this d
+      auto d_of = [&](int c) { return E4M3 ? c * (D / 8) + n : (c + 8 * (n / 8)) * 8 + n % 8; };
+      dst[d_of(2 * t)] = o[n][2 * r] * f;
+      dst[d_of(2 * t + 1)] = o[n][2 * r + 1] * f;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * (D / 4); i += TR::THREADS) {
+    const int r = i / (D / 4), d4 = i % (D / 4);
+    const int row = r0 + r;
+    if (row >= rows) break;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + r]);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) L += M == -INFINITY ? 0.f : s_l[w * 16 + r] * ex2(s_m[w * 16 + r] - M);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float4 u = *reinterpret_cast<const float4*>(s_o + (w * 16 + r) * D + d4 * 4);
+      a.x += u.x;
+      a.y += u.y;
+      a.z += u.z;
+      a.w += u.w;
+    }
+    const size_t at = static_cast<size_t>(s.q0 + row / p.group) * p.Hq + hkv * p.group + row % p.group;
+    if (pieces == 1) {
+      const float inv = M == -INFINITY ? 0.f : 1.f / L;
+      *reinterpret_cast<uint2*>(p.out + at * D + d4 * 4) =
+          make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+      if (p.lse != nullptr && d4 == 0) p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    } else {
+      __stcg(reinterpret_cast<float4*>(p.part_o + (at * p.nsplit + split) * D + d4 * 4), a);
+      if (d4 == 0) __stcg(p.part_ml + at * p.nsplit + split, make_float2(M, L));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the pieces of every row whose key range was split: one warp per (row,
+// query head). Launched behind the kernel that wrote them, whose end it awaits
+// on the device (programmatic dependent launch).
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnParams p) {
+  const int b = blockIdx.y;
+  const SeqView s = seq_view(p.batch, b, p.pool.page_size);
+  const int w = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int tok = w / p.Hq, h = w - tok * p.Hq;
+  int pieces = 1;
+  if (tok < s.nq) {
+    const int row = tok * p.group + h % p.group;
+    long long lo, hi;
+    unit_positions(p, s, row / p.row_tile * p.row_tile, lo, hi);
+    pieces = piece_count(p, key_range(p.sc, b, s, lo, hi, p.key_tile).nt);
+  }
+  // every thread waits, those without work too: this kernel's end has to stand for the pieces' kernel's
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (pieces == 1) return;
+  const size_t at = static_cast<size_t>(s.q0 + tok) * p.Hq + h;
+  const float2* ml = p.part_ml + at * p.nsplit;
+  float M = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) M = fmaxf(M, __ldcg(ml + i).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  constexpr int V = D / 32;  // elements per lane
+  float L = 0.f, a[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) a[e] = 0.f;
+  if (M != -INFINITY) {
+    const float* src = p.part_o + at * p.nsplit * D + lane * V;
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const float2 u = __ldcg(ml + i);
+      const float f = ex2(u.x - M);
+      L += u.y * f;
+      float v[V];
+      if constexpr (V == 4) {
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(i) * D));
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+      } else {
+        const float2 q = __ldcg(reinterpret_cast<const float2*>(src + static_cast<size_t>(i) * D));
+        v[0] = q.x; v[1] = q.y;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[e] += v[e] * f;
+    }
+  }
+  const float inv = M == -INFINITY ? 0.f : 1.f / L;
+  __nv_bfloat16* dst = p.out + at * D + lane * V;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(a[0] * inv, a[1] * inv);
+  if (p.lse != nullptr && lane == 0) p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+}  // namespace ll
