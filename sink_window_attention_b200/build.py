@@ -39,7 +39,7 @@ def up_to_date() -> bool:
 # Kernels that re-split registers between warpgroups (setmaxnreg) must be
 # launched with exactly this many registers per thread, or the increase would
 # wait for registers that do not exist.
-LAUNCH_REGS = {"sink_window_attention_kernel": 168}
+LAUNCH_REGS = {"sink_window_attention_kernel": 168, "paged_prefill_kernel": 128}
 
 
 def check_register_split(ptxas_log: str) -> None:

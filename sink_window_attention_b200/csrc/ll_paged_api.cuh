@@ -3,6 +3,7 @@
 #pragma once
 
 #include "ll_paged_attention.cuh"
+#include "ll_paged_prefill.cuh"
 #include "ll_tokens.cuh"
 
 namespace {
@@ -106,7 +107,10 @@ ll_status allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
 
 // How a call's rows and keys are divided among blocks. A function of the host's
 // bounds alone, so the workspace size is known before the call.
+constexpr int kDecodeRows = 32;  // rows of a sequence and K/V head up to which the decode kernel is taken
+
 struct AttnPlan {
+  bool tiles;  // 128-row tensor-memory tiles; else 16-row warp tiles
   int row_tile, key_tile, row_tiles, chunk, nsplit;
 };
 
@@ -116,15 +120,35 @@ AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq
   const long long max_q = t->max_q < t->total_q ? t->max_q : t->total_q;
   const long long cap = static_cast<long long>(t->max_pages) * c->page_size;
   const long long max_kv = t->max_kv < cap ? t->max_kv : cap;
-  a.row_tile = 16;
-  a.key_tile = 16;
+  a.tiles = max_q * group > kDecodeRows;
+  a.row_tile = a.tiles ? 256 : 16;
+  a.key_tile = a.tiles ? 128 : 16;
   a.row_tiles = static_cast<int>((max_q * group + a.row_tile - 1) / a.row_tile);
   // at most (window and prefix only shorten a range)
   const long long nt = max_kv > 0 ? (max_kv + a.key_tile - 1) / a.key_tile : 1;
-  const long long units = static_cast<long long>(t->B) * c->H * a.row_tiles;
-  const long long slots = 3ll * num_sms();
-  long long chunk = units > 0 ? nt * units / (2 * slots) : nt;
-  if (chunk < 16) chunk = 16;
+  const long long units = static_cast<long long>(t->B) * c->H * (a.row_tiles > 0 ? a.row_tiles : 1);
+  long long chunk = nt;
+  if (!a.tiles) {
+    // about two waves of blocks, so that ragged lengths even out; no piece below 256
+    // keys (64 per warp), where the join would cost more than it saves
+    const long long slots = 3ll * num_sms();
+    chunk = nt * units / (2 * slots);
+    if (chunk < 16) chunk = 16;
+  } else {
+    // one block per SM: the number of pieces with the least waves x tiles, with 4
+    // tiles' time for a block's start and end and the join's traffic in tiles (a
+    // piece of 256 rows writes and reads 256 KB, about a seventh of a tile per SM)
+    long long best = -1;
+    for (long long n = 1; n <= 16 && n <= nt; ++n) {
+      const long long per = (nt + n - 1) / n;
+      const long long waves = (units * n + num_sms() - 1) / num_sms();
+      const long long cost = 100 * waves * (per + 4) + (n > 1 ? 200 + 20 * waves : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        chunk = per;
+      }
+    }
+  }
   a.chunk = static_cast<int>(chunk < nt ? chunk : nt);
   a.nsplit = static_cast<int>((nt + a.chunk - 1) / a.chunk);
   return a;
@@ -144,6 +168,23 @@ ll_status launch_paged_decode(const ll::PagedAttnParams& p, cudaStream_t s) {
   if (st != LL_OK) return st;
   kern<<<dim3(p.nsplit * p.row_tiles, p.pool.H, p.batch.B), TR::THREADS, TR::SMEM, s>>>(p);
   return check_launch("paged_decode_kernel");
+}
+
+template <class TR, bool MODS>
+ll_status launch_paged_prefill(const ll::PagedAttnParams& p, cudaStream_t s) {
+  auto kern = ll::paged_prefill_kernel<TR, MODS>;
+  static std::atomic<unsigned long long> done{0};
+  ll_status st = allow_smem(kern, TR::SMEM, done);
+  if (st != LL_OK) return st;
+  kern<<<dim3(p.nsplit * p.row_tiles, p.pool.H, p.batch.B), TR::THREADS, TR::SMEM, s>>>(p);
+  return check_launch("paged_prefill_kernel");
+}
+
+template <int D, bool E4M3>
+ll_status launch_paged(const AttnPlan& plan, const ll::PagedAttnParams& p, cudaStream_t s) {
+  if (!plan.tiles) return launch_paged_decode<ll::DecodeTraits<D, E4M3>>(p, s);
+  using TR = ll::PrefillTraits<D, E4M3>;
+  return p.sc.cap2 > 0.f || p.sc.biased ? launch_paged_prefill<TR, true>(p, s) : launch_paged_prefill<TR, false>(p, s);
 }
 
 // The join starts while the pieces' kernel drains and waits for its end on the
@@ -373,9 +414,9 @@ ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->dtype == LL_FP8_E4M3;
   if (cache->D == 128)
-    st = e4m3 ? launch_paged_decode<ll::DecodeTraits<128, true>>(p, s) : launch_paged_decode<ll::DecodeTraits<128, false>>(p, s);
+    st = e4m3 ? launch_paged<128, true>(plan, p, s) : launch_paged<128, false>(plan, p, s);
   else
-    st = e4m3 ? launch_paged_decode<ll::DecodeTraits<64, true>>(p, s) : launch_paged_decode<ll::DecodeTraits<64, false>>(p, s);
+    st = e4m3 ? launch_paged<64, true>(plan, p, s) : launch_paged<64, false>(plan, p, s);
   if (st != LL_OK || p.nsplit == 1) return st;
   return cache->D == 128 ? launch_paged_join<128>(p, s) : launch_paged_join<64>(p, s);
 }

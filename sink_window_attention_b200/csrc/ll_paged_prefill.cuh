@@ -1,0 +1,582 @@
+// ll_paged_prefill.cuh — attention of many rows (prompts, chunks) over a paged
+// pool on the tcgen05 tensor cores.
+//
+// One CTA: up to 256 rows (token, query head of the group) of a sequence and K/V
+// head as two tiles of 128, against a piece of its keys in tiles of 128.
+//  * warps 0-3 gather K and V tiles out of the pages into a ring of shared-memory
+//    buffers in the 128-byte-swizzled operand layout, K_0 V_0 K_1 V_1 ...: a BF16
+//    pool by cp.async, an 8-bit one through registers, where E4M3 becomes fp16
+//    (exact). Plain loads rather than TMA boxes because a key tile is 1 to 8
+//    pages, rows that nobody sees are left out (read as zeros) row by row, and the
+//    8-bit tile has to pass through registers anyhow.
+//  * warp 4 issues the MMAs: S_w = Q_w K_i^T (both operands in shared memory) and
+//    O_w += P_w V_i (P in tensor memory, over S_w's columns), for the row tiles
+//    w = A, B in turn, so one tile's softmax runs under the other's MMAs.
+//  * warps 8-11 and 12-15 are A's and B's softmax, a row per thread: maxima and
+//    sums in fp32; O is rescaled in tensor memory only when the reference is
+//    exceeded by 2^8.
+// 8-bit pools: a group of 16 keys lies in one page, so its K scale is a factor and
+// the exponent of its V scale an offset per 16 scores; the V scale's mantissa (1
+// for the powers of two that the append writes) is multiplied into V's fp16.
+#pragma once
+
+#include "ll_paged_attention.cuh"
+
+namespace ll {
+
+template <int D_, bool E4M3_>
+struct PrefillTraits {
+  static constexpr int D = D_;
+  static constexpr bool E4M3 = E4M3_;
+  static constexpr int BM = 128, BN = 128;
+  static constexpr int NB = D / 64;              // 128-byte column blocks of a row
+  static constexpr int TILE = BN * D * 2;        // one K, V or Q operand tile
+  static constexpr int CTRL = 2048;
+  static constexpr int STAGES = (232448 - CTRL - 1024 - 2 * TILE) / TILE < 8
+                                    ? (232448 - CTRL - 1024 - 2 * TILE) / TILE : 8;
+  static constexpr int SMEM = CTRL + 1024 + (2 + STAGES) * TILE;
+  // Slots of per-tile page data. Slot i is written again with buffer K_(i+META),
+  // which can only be filled once V_i was consumed (2 META - STAGES >= 1), that is
+  // after both softmax warpgroups handed over P_i and so have read slot i.
+  static constexpr int META = STAGES / 2 + 1;
+  static_assert(2 * META - STAGES >= 1, "meta slots");
+  static constexpr int THREADS = 512;
+  // registers: launch 128 per thread (512 x 128 = 65536); loaders 88, the MMA
+  // issuer's warpgroup 40, the softmax warpgroups 192: 88 + 40 + 2 x 192 = 4 x 128
+  static constexpr int LAUNCH_REGS = 128, REGS_LOAD = 88, REGS_MMA = 40, REGS_SOFTMAX = 192;
+  static_assert(REGS_LOAD + REGS_MMA + 2 * REGS_SOFTMAX <= 4 * LAUNCH_REGS, "register split exceeds the launch");
+  static constexpr int TMEM_COLS = 512, S_COL = 0, O_COL = 2 * BN;
+  static constexpr int FMT = E4M3 ? 0 : 1;       // kind::f16 operands: f16 or bf16
+  static_assert(STAGES >= 5, "the issue order needs five buffers");
+};
+
+// What the softmax has to know of 16 keys that lie in one page.
+struct KeyGroup {
+  float ks;      // K scale
+  float c;       // exponent of the V scale
+  float inv_c;   // 2^-c
+  float mapped;  // 0: the table names no page
+};
+
+// Like turn_of, with the hardware's sine and cosine of at most an eighth of a
+// turn (within 2^-21): for queries, which are rounded to 16 bits right after.
+__device__ __forceinline__ float2 turn_fast(const TokenRope& r, long long pos, int i) {
+  const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * r.turns[i]) >> 32);
+  const uint32_t quarter = (t + 0x20000000u) >> 30;
+  const float a = static_cast<float>(static_cast<int>(t - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  float s, c;
+  __sincosf(a, &s, &c);
+  float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+  if ((quarter + 1) & 2) x = -x;
+  if (quarter & 2) y = -y;
+  return make_float2(x * r.amp, y * r.amp);
+}
+
+template <class TR, bool MODS>
+__global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const PagedAttnParams p) {
+  constexpr int D = TR::D, BM = TR::BM, BN = TR::BN, STAGES = TR::STAGES, TILE = TR::TILE;
+  constexpr bool E4M3 = TR::E4M3;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                 // [2][TILE]
+  uint8_t* sKV = smem + 2 * TILE;     // [STAGES][TILE]
+  uint8_t* ctrl = sKV + STAGES * TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);  // [STAGES]
+  uint64_t* empty = full + 8;                          // [STAGES]
+  uint64_t* meta_full = empty + 8;                     // [META]
+  uint64_t* q_full = meta_full + TR::META;
+  uint64_t* s_full = q_full + 1;   // [2]
+  uint64_t* p_ready = s_full + 2;  // [2]
+  uint64_t* o_done = p_ready + 2;  // [2]
+  uint64_t* drain = o_done + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  KeyGroup* meta = reinterpret_cast<KeyGroup*>(ctrl + 512);  // [META][8]
+  static_assert((8 + 8 + TR::META + 8) * 8 + 8 <= 512 && 512 + TR::META * 8 * sizeof(KeyGroup) <= TR::CTRL, "control block");
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  // the last rows of a sequence see the most keys: they start first
+  const int rt = p.row_tiles - 1 - blockIdx.x % p.row_tiles, split = blockIdx.x / p.row_tiles;
+  const int hkv = blockIdx.y, b = blockIdx.z;
+  const int ps = p.pool.page_size;
+  const SeqView s = seq_view(p.batch, b, ps);
+  const int rows = s.nq * p.group, r0 = rt * 2 * BM;
+  if (r0 >= rows) return;
+  long long p_lo, p_hi;
+  unit_positions(p, s, r0, p_lo, p_hi);
+  const KeyRange kr = key_range(p.sc, b, s, p_lo, p_hi, BN);
+  const int pieces = piece_count(p, kr.nt);
+  if (split >= pieces) return;
+  const int t_beg = split * p.chunk;
+  const int n = min(kr.nt, t_beg + p.chunk) - t_beg;  // key tiles of this piece (0: nothing is seen)
+  const bool two = rows - r0 > BM;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], 128);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < TR::META; ++i) mbar_init(&meta_full[i], 1);
+    mbar_init(q_full, two ? 256 : 128);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&s_full[w], 1);
+      mbar_init(&p_ready[w], 128);
+      mbar_init(&o_done[w], 1);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(s_tmem, TR::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *s_tmem;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ loaders
+    regs_dec<TR::REGS_LOAD>();
+    const int tid = threadIdx.x;
+    // lane g < 8 holds the page of keys [16 g, 16 g + 16) of a tile (-1: none)
+    auto page_for = [&](int i) -> int {
+      if (lane >= 8 || i >= n) return -1;
+      const int key = kr.tile(t_beg + i) * BN + lane * 16;
+      return key < s.len ? page_of(p.batch, b, key / ps, p.pool.n_pages) : -1;
+    };
+    auto scale_for = [&](const float* scales, int page) -> float {
+      return E4M3 && page >= 0 ? scales[static_cast<size_t>(page) * p.pool.H + hkv] : 0.f;
+    };
+    int pg = page_for(0), pg1 = page_for(1);
+    float ks = scale_for(p.pool.k_scale, pg), vs = scale_for(p.pool.v_scale, pg);
+    bool ok = true;
+    // every loader thread's writes of buffer `pos` are done
+    auto publish = [&](int pos) {
+      fence_proxy_async_smem();
+      mbar_arrive(&full[pos % STAGES]);
+    };
+    auto wait_empty = [&](int pos) {
+      if (ok) ok = mbar_wait(&empty[pos % STAGES], ((pos / STAGES) & 1) ^ 1, s_abort);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    auto put_meta = [&](int i) {
+      if (warp == 0) {
+        if (lane < 8) {
+          const float c = E4M3 ? scale_exponent(vs) : 0.f;
+          meta[(i % TR::META) * 8 + lane] = KeyGroup{E4M3 ? ks : 1.f, c, exp2f(-c), pg >= 0 ? 1.f : 0.f};
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&meta_full[i % TR::META]);
+      }
+    };
+    if constexpr (!E4M3) {
+      constexpr int CPR = D / 8, RPS = 128 / CPR, STEPS = BN / RPS;  // chunks per row, rows per step
+      constexpr int AHEAD = 2;  // buffers in flight behind the one being issued
+      const int c = tid % CPR, r = tid / CPR;
+      const uint32_t dst0 = smem_addr(sKV) + (c >> 3) * (BN * 128);
+      int done = 0;
+      for (int i = 0; i < n && ok; ++i) {
+        const int pg2 = page_for(i + 2);
+        const int key0 = kr.tile(t_beg + i) * BN;
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const int pos = 2 * i + kv;
+          wait_empty(pos);
+          if (!ok) break;
+          const uint8_t* src = static_cast<const uint8_t*>(kv ? p.pool.v : p.pool.k) + c * 16;
+          const uint32_t dst = dst0 + (pos % STAGES) * TILE;
+#pragma unroll 8
+          for (int k = 0; k < STEPS; ++k) {
+            const int row = r + k * RPS;
+            const int page = __shfl_sync(0xffffffffu, pg, row >> 4);
+            const bool valid = page >= 0 && kr.some_row_sees(key0 + row);
+            const size_t at = ((static_cast<size_t>(valid ? page : 0) * p.pool.H + hkv) * ps + ((key0 + row) & (ps - 1))) *
+                              (D * 2);
+            cp_async16(dst + sw128_offset(row, c & 7), src + at, valid);
+          }
+          cp_async_commit();
+          if (kv == 0) put_meta(i);
+          if (pos >= AHEAD) {
+            cp_async_wait<AHEAD>();
+            publish(pos - AHEAD);
+            done = pos - AHEAD + 1;
+          }
+        }
+        pg = pg1;
+        pg1 = pg2;
+      }
+      cp_async_wait<0>();
+      if (ok)
+        for (; done < 2 * n; ++done) publish(done);
+    } else {
+      constexpr int CPR = D / 16, RPS = 128 / CPR, STEPS = BN / RPS;  // 16-code chunks per row
+      const int c = tid % CPR;
+      // the upper half of a row's chunks lies 128 rows x 128 bytes further on, in the
+      // same banks: those lanes take the neighbouring row, whose chunks are permuted
+      // to the other banks
+      const int r = (tid / CPR) ^ (CPR == 8 ? c >> 2 : 0);
+      uint4 buf[STEPS];
+      auto load_step = [&](int kv, int key0, int pages, int k) -> uint4 {
+        const int row = r + k * RPS;
+        const int page = __shfl_sync(0xffffffffu, pages, row >> 4);
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (page >= 0 && kr.some_row_sees(key0 + row)) {
+          const uint8_t* src = static_cast<const uint8_t*>(kv ? p.pool.v : p.pool.k) +
+                               ((static_cast<size_t>(page) * p.pool.H + hkv) * ps + ((key0 + row) & (ps - 1))) * D + c * 16;
+          u = __ldg(reinterpret_cast<const uint4*>(src));
+        }
+        return u;
+      };
+      if (n > 0) {
+        const int key0 = kr.tile(t_beg) * BN;
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) buf[k] = load_step(0, key0, pg, k);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const int pg2 = page_for(i + 2);
+        const float ks1 = scale_for(p.pool.k_scale, pg1), vs1 = scale_for(p.pool.v_scale, pg1);
+        const int key0 = kr.tile(t_beg + i) * BN;
+        const int key1 = i + 1 < n ? kr.tile(t_beg + i + 1) * BN : 0;
+        // V's scale without its exponent, for the 16 keys of lane g
+        const float vc = scale_exponent(vs);
+        const float mant = vs * exp2f(-vc);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int pos = 2 * i + kv;
+          wait_empty(pos);
+          if (!ok) break;
+          uint8_t* dst = sKV + (pos % STAGES) * TILE + (c >> 2) * (BN * 128);
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k) {
+            const int row = r + k * RPS;
+            const uint32_t w[4] = {buf[k].x, buf[k].y, buf[k].z, buf[k].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[2 * e] = e4m3x2_f16(w[e]);
+              h[2 * e + 1] = e4m3x2_f16(w[e] >> 16);
+            }
+            if (kv) {
+              const float f = __shfl_sync(0xffffffffu, mant, row >> 4);
+              if (f != 1.f) {  // a scale that is no power of two
+                const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[e]), f2);
+                  h[e] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+              }
+            }
+            *reinterpret_cast<uint4*>(dst + sw128_offset(row, (2 * c) & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + sw128_offset(row, (2 * c + 1) & 7)) = make_uint4(h[4], h[5], h[6], h[7]);
+            // the same step of the next buffer takes these registers
+            if (kv == 0) buf[k] = load_step(1, key0, pg, k);
+            else if (i + 1 < n) buf[k] = load_step(0, key1, pg1, k);
+          }
+          if (kv == 0) put_meta(i);
+          publish(pos);
+        }
+        pg = pg1;
+        pg1 = pg2;
+        ks = ks1;
+        vs = vs1;
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ MMA issuer
+    regs_dec<TR::REGS_MMA>();
+    if (warp == 4 && lane == 0 && n > 0) {
+      constexpr uint32_t idS = idesc_dense(BM, BN, TR::FMT, false, false);
+      constexpr uint32_t idO = idesc_dense(BM, D, TR::FMT, false, true);
+      const DescWords dQ = desc_words(smem_addr(sQ), 16, 1024, 2), dK = desc_words(smem_addr(sKV), 16, 1024, 2);
+      const DescWords dV = desc_words(smem_addr(sKV), BN * 128, 1024, 2);
+      auto wait_full = [&](int pos) { return mbar_wait(&full[pos % STAGES], (pos / STAGES) & 1, s_abort); };
+      auto issue_s = [&](int w, int i) {
+        const uint32_t koff = ((2 * i) % STAGES) * TILE;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * (BM * 128) + (k & 3) * 32;
+          mma_bf16_ss(tbase + TR::S_COL + w * BN, desc_at(dQ, w * TILE + off), desc_at(dK, koff + off), idS, k > 0);
+        }
+        mma_commit(&s_full[w]);
+      };
+      auto issue_pv = [&](int w, int i) {
+        const uint32_t voff = ((2 * i + 1) % STAGES) * TILE;
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_bf16_ts(tbase + TR::O_COL + w * D, tbase + TR::S_COL + w * BN + k * 8, desc_at(dV, voff + k * 16 * 128),
+                      idO, i > 0 || k > 0);
+        if (i == n - 1) mma_commit(&o_done[w]);
+      };
+      bool ok = mbar_wait(q_full, 0, s_abort) && wait_full(0);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        if (two) issue_s(1, 0);
+        mma_commit(&empty[0]);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        if (!(ok = wait_full(2 * i + 1) && mbar_wait(&p_ready[0], i & 1, s_abort))) break;
+        tc_fence_after();
+        issue_pv(0, i);
+        if (i + 1 < n) {
+          if (!(ok = wait_full(2 * i + 2))) break;
+          issue_s(0, i + 1);
+        }
+        if (two) {
+          if (!(ok = mbar_wait(&p_ready[1], i & 1, s_abort))) break;
+          tc_fence_after();
+          issue_pv(1, i);
+        }
+        mma_commit(&empty[(2 * i + 1) % STAGES]);
+        if (i + 1 < n) {
+          if (two) issue_s(1, i + 1);
+          mma_commit(&empty[(2 * i + 2) % STAGES]);
+        }
+      }
+      mma_commit(drain);
+      mbar_wait_teardown(drain, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_inc<TR::REGS_SOFTMAX>();
+    const int w = (warp - 8) >> 2;
+    const int row = (threadIdx.x - 256) & 127;  // TMEM lane
+    const int ur = r0 + w * BM + row;           // row of the unit's sequence and head
+    const bool live = ur < rows;
+    if (w == 0 || two) {
+      const int tok = ur / p.group, h = hkv * p.group + ur % p.group;
+      const long long pos = s.first_pos + tok;
+      // ---- this row of Q, rotated, into the operand layout
+      float qf = 1.f;
+      {
+        const __nv_bfloat16* src = p.q + static_cast<long long>(s.q0 + (live ? tok : 0)) * p.q_stride + h * D;
+        uint8_t* dst = sQ + w * TILE;
+        float inv = 1.f;
+        if constexpr (E4M3) {  // fp16 under a power of two (see the decode kernel); a rotated element is below 2 amp max
+          float a = 0.f;
+          if (live)
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+              float x[8];
+              load_chunk8<__nv_bfloat16>(src + c * 8, x);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
+            }
+          if (p.rope.rot > 0) a *= fmaxf(fabsf(p.rope.amp), 1.f);
+          qf = power_below(a);
+          inv = 1.f / qf;
+        }
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {
+          int lo, hi;
+          item_chunks(p.rope, c, lo, hi);
+          float x[8], y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+          if (live) {
+            load_chunk8<__nv_bfloat16>(src + lo * 8, x);
+            load_chunk8<__nv_bfloat16>(src + hi * 8, y);
+            if (c < (p.rope.rot >> 4)) {
+              float2 cs[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) cs[e] = turn_fast(p.rope, pos, c * 8 + e);
+              rotate_item(p.rope, x, y, cs);
+            }
+          }
+          uint32_t u[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            u[e] = E4M3 ? pack_f16(x[2 * e] * inv, x[2 * e + 1] * inv) : pack_bf16(x[2 * e], x[2 * e + 1]);
+            u[4 + e] = E4M3 ? pack_f16(y[2 * e] * inv, y[2 * e + 1] * inv) : pack_bf16(y[2 * e], y[2 * e + 1]);
+          }
+          *reinterpret_cast<uint4*>(dst + (lo >> 3) * (BM * 128) + sw128_offset(row, lo & 7)) =
+              make_uint4(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint4*>(dst + (hi >> 3) * (BM * 128) + sw128_offset(row, hi & 7)) =
+              make_uint4(u[4], u[5], u[6], u[7]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+      }
+      // ---- the keys this row sees: [0, sees_a) and [sees_b, sees_e)
+      int sees_a = 0, sees_b = 0, sees_e = 0;
+      if (live) {
+        const long long e = pos + 1 < s.len ? pos + 1 : s.len;
+        sees_e = static_cast<int>(e > 0 ? e : 0);
+        const long long lo = p.sc.window > 0 ? pos - p.sc.window + 1 : 0;
+        sees_b = static_cast<int>(lo < 0 ? 0 : (lo < sees_e ? lo : sees_e));
+        const int sink = p.sc.window > 0 ? min(p.sc.n_sink, sees_e) : 0;
+        sees_a = max(kr.prefix, sink);
+      }
+      // positions of this tile's first and last row, for tiles that need no mask
+      const long long w_lo = s.first_pos + (r0 + w * BM) / p.group;
+      const long long w_hi = s.first_pos + (min(r0 + w * BM + BM, rows) - 1) / p.group;
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t tS = tbase + lane_off + TR::S_COL + w * BN;
+      const uint32_t tO = tbase + lane_off + TR::O_COL + w * D;
+      const float fac = qf * p.sc.pre;
+      const float slope = MODS && p.sc.biased ? p.sc.slope2[h] : 0.f;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int i = 0; i < n; ++i) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&meta_full[i % TR::META], (i / TR::META) & 1, s_abort));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], i & 1, s_abort));
+        if (!ok) break;
+        tc_fence_after();
+        const KeyGroup* kg = meta + (i % TR::META) * 8;
+        const int key0 = kr.tile(t_beg + i) * BN;
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load32(tS + c * 32, sr[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load_wait(sr[c]);
+        bool mapped = true;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) mapped = mapped && kg[g].mapped != 0.f;
+        const bool all_seen = mapped && (key0 + BN <= kr.prefix ||
+                                         (key0 + BN - 1 <= w_lo && key0 + BN <= s.len &&
+                                          (p.sc.window == 0 || w_hi - key0 < p.sc.window)));
+        if constexpr (MODS) {
+          const float pj = static_cast<float>(pos - key0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float x = score2(p.sc, __uint_as_float(sr[c][e]), E4M3 ? fac * kg[2 * c + (e >> 4)].ks : fac);
+              x -= slope * fabsf(pj - static_cast<float>(c * 32 + e));
+              sr[c][e] = __float_as_uint(x);
+            }
+        }
+        if (!all_seen) {
+          const int a = sees_a - key0, bb = sees_b - key0, ee = sees_e - key0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int j = c * 32 + e;
+              const bool seen = (j < a || (j >= bb && j < ee)) && kg[2 * c + (e >> 4)].mapped != 0.f;
+              if (!seen) sr[c][e] = __float_as_uint(-INFINITY);
+            }
+        }
+        // factor on the scores of group g (kept off 0, so that masked ones stay -inf)
+        auto factor = [&](int g) { return MODS ? 1.f : (E4M3 ? fmaxf(fac * kg[g].ks, 1e-37f) : fac); };
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float q[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            q[e & 3] = fmax3(q[e & 3], __uint_as_float(sr[g >> 1][(g & 1) * 16 + 2 * e]),
+                             __uint_as_float(sr[g >> 1][(g & 1) * 16 + 2 * e + 1]));
+          const float x = fmaxf(fmax3(q[0], q[1], q[2]), q[3]);
+          mx = E4M3 ? fmaxf(mx, fmaf(x, factor(g), kg[g].c)) : fmaxf(mx, x);
+        }
+        if (!E4M3) mx *= factor(0);
+        const bool raise = mx > m + 8.f;
+        const float m_use = raise ? mx : m;
+        if (__any_sync(0xffffffffu, raise) && i > 0) {
+          const float al = raise ? ex2(m - m_use) : 1.f;
+          l *= al;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_load32(tO + c * 32, o);
+            tmem_load_wait(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+            tmem_store32(tO + c * 32, o);
+          }
+        }
+        m = m_use;
+        const float ms = m == -INFINITY ? 0.f : m;
+        uint64_t l2 = 0ull;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int g = 2 * c + hf;
+            const float f = factor(g), off = E4M3 ? kg[g].c - ms : -ms;
+            const uint64_t f2 = f2_pack(f, f), off2 = f2_pack(off, off);
+            uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int at = hf * 16 + 2 * e;
+              const uint64_t x2 =
+                  f2_fma(f2_pack(__uint_as_float(sr[c][at]), __uint_as_float(sr[c][at + 1])), f2, off2);
+              float x0, x1;
+              f2_unpack(x2, x0, x1);
+              const float e0 = ex2(x0), e1 = ex2(x1);
+              part[e & 1] = f2_add(part[e & 1], f2_pack(e0, e1));
+              sr[c][hf * 8 + e] = E4M3 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+            }
+            const uint64_t sum = f2_add(part[0], part[1]);
+            if constexpr (E4M3) l2 = f2_fma(sum, f2_pack(kg[g].inv_c, kg[g].inv_c), l2);
+            else l2 = f2_add(l2, sum);
+          }
+          tmem_store16(tS + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&sr[c][0]));
+        }
+        float u0, u1;
+        f2_unpack(l2, u0, u1);
+        l += u0 + u1;
+        tmem_store_wait();
+        tc_fence_before();
+        mbar_arrive(&p_ready[w]);
+      }
+      // ---- epilogue
+      if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[w], 0, s_abort));
+      tc_fence_after();
+      if (ok) {
+        const size_t at = static_cast<size_t>(s.q0 + tok) * p.Hq + h;
+        const bool none = m == -INFINITY;
+        const float inv = none ? 0.f : 1.f / l;
+        if (pieces == 1) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            if (n > 0) {
+              tmem_load32(tO + c * 32, o);
+              tmem_load_wait(o);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t u[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                u[e] = none ? 0u : pack_bf16(__uint_as_float(o[q * 8 + 2 * e]) * inv, __uint_as_float(o[q * 8 + 2 * e + 1]) * inv);
+              if (live) dst[q] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+            __syncwarp();
+          }
+          if (live && p.lse != nullptr) p.lse[at] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_load32(tO + c * 32, o);
+            tmem_load_wait(o);
+            float4* dst = reinterpret_cast<float4*>(p.part_o + (at * p.nsplit + split) * D + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (live)
+                __stcg(dst + q, none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                     : make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                                   __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3])));
+            __syncwarp();
+          }
+          if (live) __stcg(p.part_ml + at * p.nsplit + split, make_float2(m, l));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tbase, TR::TMEM_COLS);
+  }
+}
+
+}  // namespace ll
