@@ -43,6 +43,9 @@ ll_status check_paged_cache(const ll_paged_cache* c) {
     return fail(LL_ERR_INVALID_ARG, "page_size = %d must be 16, 32, 64 or 128", c->page_size);
   if (c->D != 64 && c->D != 128) return fail(LL_ERR_INVALID_ARG, "D = %d must be 64 or 128", c->D);
   if (c->H > LL_MAX_TOKEN_HEADS) return fail(LL_ERR_INVALID_ARG, "H = %d exceeds %d", c->H, LL_MAX_TOKEN_HEADS);
+  if (static_cast<long long>(c->n_pages) * c->H * (c->page_size / 16) > INT_MAX)
+    return fail(LL_ERR_INVALID_ARG, "n_pages x H x page_size / 16 = %lld exceeds 2^31 - 1",
+                static_cast<long long>(c->n_pages) * c->H * (c->page_size / 16));
   return LL_OK;
 }
 

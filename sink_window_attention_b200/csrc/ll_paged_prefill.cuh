@@ -41,9 +41,9 @@ struct PrefillTraits {
   static constexpr int META = STAGES / 2 + 1;
   static_assert(2 * META - STAGES >= 1, "meta slots");
   static constexpr int THREADS = 512;
-  // registers: launch 128 per thread (512 x 128 = 65536); loaders 88, the MMA
-  // issuer's warpgroup 40, the softmax warpgroups 192: 88 + 40 + 2 x 192 = 4 x 128
-  static constexpr int LAUNCH_REGS = 128, REGS_LOAD = 88, REGS_MMA = 40, REGS_SOFTMAX = 192;
+  // registers: launch 128 per thread (512 x 128 = 65536); loaders 80, the MMA
+  // issuer's warpgroup 48, the softmax warpgroups 192: 80 + 48 + 2 x 192 = 4 x 128
+  static constexpr int LAUNCH_REGS = 128, REGS_LOAD = 80, REGS_MMA = 48, REGS_SOFTMAX = 192;
   static_assert(REGS_LOAD + REGS_MMA + 2 * REGS_SOFTMAX <= 4 * LAUNCH_REGS, "register split exceeds the launch");
   static constexpr int TMEM_COLS = 512, S_COL = 0, O_COL = 2 * BN;
   static constexpr int FMT = E4M3 ? 0 : 1;       // kind::f16 operands: f16 or bf16
@@ -141,11 +141,16 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
     // ------------------------------------------------------------ loaders
     regs_dec<TR::REGS_LOAD>();
     const int tid = threadIdx.x;
-    // lane g < 8 holds the page of keys [16 g, 16 g + 16) of a tile (-1: none)
+    // Lane g < 8 holds the place of keys [16 g, 16 g + 16) of a tile, which lie in
+    // one page: their page (-1: none) and their number in the pool's runs of 16 rows.
+    const int per_page = ps >> 4;
     auto page_for = [&](int i) -> int {
       if (lane >= 8 || i >= n) return -1;
       const int key = kr.tile(t_beg + i) * BN + lane * 16;
       return key < s.len ? page_of(p.batch, b, key / ps, p.pool.n_pages) : -1;
+    };
+    auto run_of = [&](int i, int page) -> int {
+      return page < 0 ? -1 : (page * p.pool.H + hkv) * per_page + ((kr.tile(t_beg + i) * 8 + lane) & (per_page - 1));
     };
     auto scale_for = [&](const float* scales, int page) -> float {
       return E4M3 && page >= 0 ? scales[static_cast<size_t>(page) * p.pool.H + hkv] : 0.f;
@@ -153,13 +158,13 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
     int pg = page_for(0), pg1 = page_for(1);
     float ks = scale_for(p.pool.k_scale, pg), vs = scale_for(p.pool.v_scale, pg);
     bool ok = true;
-    // every loader thread's writes of buffer `pos` are done
-    auto publish = [&](int pos) {
+    // this thread's writes of buffer `pos` are done
+    auto publish = [&](int st) {
       fence_proxy_async_smem();
-      mbar_arrive(&full[pos % STAGES]);
+      mbar_arrive(&full[st]);
     };
-    auto wait_empty = [&](int pos) {
-      if (ok) ok = mbar_wait(&empty[pos % STAGES], ((pos / STAGES) & 1) ^ 1, s_abort);
+    auto wait_empty = [&](int st, int round) {
+      if (ok) ok = mbar_wait(&empty[st], (round & 1) ^ 1, s_abort);
       ok = __all_sync(0xffffffffu, ok);
     };
     auto put_meta = [&](int i) {
@@ -172,44 +177,57 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         if (lane == 0) mbar_arrive(&meta_full[i % TR::META]);
       }
     };
+    // every row of a tile is seen by some row of the unit: nothing to leave out
+    auto whole_tile = [&](int key0) { return key0 + BN <= kr.always || (key0 >= kr.lo && key0 + BN <= kr.upper); };
+    int st = 0, round = 0;  // buffer and its use
     if constexpr (!E4M3) {
-      constexpr int CPR = D / 8, RPS = 128 / CPR, STEPS = BN / RPS;  // chunks per row, rows per step
+      constexpr int CPR = D / 8, RPS = 128 / CPR, PER_RUN = 16 / RPS;  // chunks per row, rows per step, steps per run
       constexpr int AHEAD = 2;  // buffers in flight behind the one being issued
       const int c = tid % CPR, r = tid / CPR;
-      const uint32_t dst0 = smem_addr(sKV) + (c >> 3) * (BN * 128);
-      int done = 0;
+      const uint32_t dst0 = smem_addr(sKV) + (c >> 3) * (BN * 128) + sw128_offset(r, c & 7);
+      const size_t lane_off = static_cast<size_t>(r) * (D * 2) + c * 16;
+      int behind = 0, behind_st = 0;  // buffers issued but not published, and the oldest of them
       for (int i = 0; i < n && ok; ++i) {
         const int pg2 = page_for(i + 2);
         const int key0 = kr.tile(t_beg + i) * BN;
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int pos = 2 * i + kv;
-          wait_empty(pos);
+        const int run = run_of(i, pg);
+        const bool whole = whole_tile(key0);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          wait_empty(st, round);
           if (!ok) break;
-          const uint8_t* src = static_cast<const uint8_t*>(kv ? p.pool.v : p.pool.k) + c * 16;
-          const uint32_t dst = dst0 + (pos % STAGES) * TILE;
-#pragma unroll 8
-          for (int k = 0; k < STEPS; ++k) {
-            const int row = r + k * RPS;
-            const int page = __shfl_sync(0xffffffffu, pg, row >> 4);
-            const bool valid = page >= 0 && kr.some_row_sees(key0 + row);
-            const size_t at = ((static_cast<size_t>(valid ? page : 0) * p.pool.H + hkv) * ps + ((key0 + row) & (ps - 1))) *
-                              (D * 2);
-            cp_async16(dst + sw128_offset(row, c & 7), src + at, valid);
+          const uint8_t* src = static_cast<const uint8_t*>(kv ? p.pool.v : p.pool.k) + lane_off;
+          const uint32_t dst = dst0 + st * TILE;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const int at = __shfl_sync(0xffffffffu, run, g);
+            const uint8_t* from = src + static_cast<size_t>(at < 0 ? 0 : at) * (16 * D * 2);
+#pragma unroll
+            for (int k = 0; k < PER_RUN; ++k) {
+              const int row = g * 16 + k * RPS;  // + r; whole 8-row swizzle atoms, so the swizzle is r's
+              const bool valid = at >= 0 && (whole || kr.some_row_sees(key0 + row + r));
+              cp_async16(dst + row * 128, from + k * (RPS * D * 2), valid);
+            }
           }
           cp_async_commit();
           if (kv == 0) put_meta(i);
-          if (pos >= AHEAD) {
+          if (++behind > AHEAD) {
             cp_async_wait<AHEAD>();
-            publish(pos - AHEAD);
-            done = pos - AHEAD + 1;
+            publish(behind_st);
+            --behind;
+            if (++behind_st == STAGES) behind_st = 0;
           }
+          if (++st == STAGES) st = 0, ++round;
         }
         pg = pg1;
         pg1 = pg2;
       }
       cp_async_wait<0>();
       if (ok)
-        for (; done < 2 * n; ++done) publish(done);
+        for (; behind > 0; --behind) {
+          publish(behind_st);
+          if (++behind_st == STAGES) behind_st = 0;
+        }
     } else {
       constexpr int CPR = D / 16, RPS = 128 / CPR, STEPS = BN / RPS;  // 16-code chunks per row
       const int c = tid % CPR;
@@ -217,40 +235,47 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       // same banks: those lanes take the neighbouring row, whose chunks are permuted
       // to the other banks
       const int r = (tid / CPR) ^ (CPR == 8 ? c >> 2 : 0);
+      const uint32_t off0 = (c >> 2) * (BN * 128) + sw128_offset(r, (2 * c) & 7);
+      const uint32_t off1 = (c >> 2) * (BN * 128) + sw128_offset(r, (2 * c + 1) & 7);
+      const size_t lane_off = static_cast<size_t>(r & 15) * D + c * 16;
       uint4 buf[STEPS];
-      auto load_step = [&](int kv, int key0, int pages, int k) -> uint4 {
-        const int row = r + k * RPS;
-        const int page = __shfl_sync(0xffffffffu, pages, row >> 4);
+      auto load_step = [&](const void* pool, int run, int key0, bool whole, int k) -> uint4 {
+        const int at = __shfl_sync(0xffffffffu, run, (r + k * RPS) >> 4);
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (page >= 0 && kr.some_row_sees(key0 + row)) {
-          const uint8_t* src = static_cast<const uint8_t*>(kv ? p.pool.v : p.pool.k) +
-                               ((static_cast<size_t>(page) * p.pool.H + hkv) * ps + ((key0 + row) & (ps - 1))) * D + c * 16;
-          u = __ldg(reinterpret_cast<const uint4*>(src));
+        if (at >= 0 && (whole || kr.some_row_sees(key0 + r + k * RPS))) {
+          const uint8_t* from = static_cast<const uint8_t*>(pool) + static_cast<size_t>(at) * (16 * D) + lane_off;
+          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                       : "l"(from));
         }
         return u;
       };
+      int key0 = n > 0 ? kr.tile(t_beg) * BN : 0, run = run_of(0, pg);
+      bool whole = whole_tile(key0);
       if (n > 0) {
-        const int key0 = kr.tile(t_beg) * BN;
 #pragma unroll
-        for (int k = 0; k < STEPS; ++k) buf[k] = load_step(0, key0, pg, k);
+        for (int k = 0; k < STEPS; ++k) buf[k] = load_step(p.pool.k, run, key0, whole, k);
       }
       for (int i = 0; i < n && ok; ++i) {
         const int pg2 = page_for(i + 2);
         const float ks1 = scale_for(p.pool.k_scale, pg1), vs1 = scale_for(p.pool.v_scale, pg1);
-        const int key0 = kr.tile(t_beg + i) * BN;
-        const int key1 = i + 1 < n ? kr.tile(t_beg + i + 1) * BN : 0;
         // V's scale without its exponent, for the 16 keys of lane g
-        const float vc = scale_exponent(vs);
-        const float mant = vs * exp2f(-vc);
-#pragma unroll
+        const float mant = vs * exp2f(-scale_exponent(vs));
+        const bool plain = __all_sync(0xffffffffu, lane >= 8 || mant == 1.f);
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          const int pos = 2 * i + kv;
-          wait_empty(pos);
+          wait_empty(st, round);
           if (!ok) break;
-          uint8_t* dst = sKV + (pos % STAGES) * TILE + (c >> 2) * (BN * 128);
+          uint8_t* dst = sKV + st * TILE;
+          if (kv == 1 && i + 1 < n) {  // the registers that this buffer frees take the next one
+            key0 = kr.tile(t_beg + i + 1) * BN;
+            run = run_of(i + 1, pg1);
+            whole = whole_tile(key0);
+          }
+          const void* next = kv == 0 ? p.pool.v : p.pool.k;
+          const bool more = kv == 0 || i + 1 < n;
 #pragma unroll
           for (int k = 0; k < STEPS; ++k) {
-            const int row = r + k * RPS;
             const uint32_t w[4] = {buf[k].x, buf[k].y, buf[k].z, buf[k].w};
             uint32_t h[8];
 #pragma unroll
@@ -258,25 +283,21 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
               h[2 * e] = e4m3x2_f16(w[e]);
               h[2 * e + 1] = e4m3x2_f16(w[e] >> 16);
             }
-            if (kv) {
-              const float f = __shfl_sync(0xffffffffu, mant, row >> 4);
-              if (f != 1.f) {  // a scale that is no power of two
-                const __half2 f2 = __float2half2_rn(f);
+            if (kv && !plain) {  // a scale that is no power of two
+              const __half2 f2 = __float2half2_rn(__shfl_sync(0xffffffffu, mant, (r + k * RPS) >> 4));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[e]), f2);
-                  h[e] = *reinterpret_cast<const uint32_t*>(&y);
-                }
+              for (int e = 0; e < 8; ++e) {
+                const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[e]), f2);
+                h[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
             }
-            *reinterpret_cast<uint4*>(dst + sw128_offset(row, (2 * c) & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(dst + sw128_offset(row, (2 * c + 1) & 7)) = make_uint4(h[4], h[5], h[6], h[7]);
-            // the same step of the next buffer takes these registers
-            if (kv == 0) buf[k] = load_step(1, key0, pg, k);
-            else if (i + 1 < n) buf[k] = load_step(0, key1, pg1, k);
+            *reinterpret_cast<uint4*>(dst + off0 + k * (RPS * 128)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + off1 + k * (RPS * 128)) = make_uint4(h[4], h[5], h[6], h[7]);
+            if (more) buf[k] = load_step(next, run, key0, whole, k);
           }
           if (kv == 0) put_meta(i);
-          publish(pos);
+          publish(st);
+          if (++st == STAGES) st = 0, ++round;
         }
         pg = pg1;
         pg1 = pg2;
@@ -290,50 +311,64 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
     if (warp == 4 && lane == 0 && n > 0) {
       constexpr uint32_t idS = idesc_dense(BM, BN, TR::FMT, false, false);
       constexpr uint32_t idO = idesc_dense(BM, D, TR::FMT, false, true);
-      const DescWords dQ = desc_words(smem_addr(sQ), 16, 1024, 2), dK = desc_words(smem_addr(sKV), 16, 1024, 2);
-      const DescWords dV = desc_words(smem_addr(sKV), BN * 128, 1024, 2);
-      auto wait_full = [&](int pos) { return mbar_wait(&full[pos % STAGES], (pos / STAGES) & 1, s_abort); };
-      auto issue_s = [&](int w, int i) {
-        const uint32_t koff = ((2 * i) % STAGES) * TILE;
+      // The descriptors' high words are constants; the low ones are kept from being
+      // hoisted out of the loop (`opaque`): hundreds of them would live in local memory.
+      const uint32_t hi = desc_words(0, 0, 1024, 2).hi;
+      const uint32_t q_lo = desc_words(smem_addr(sQ), 16, 1024, 2).lo;
+      const uint32_t k_lo = desc_words(smem_addr(sKV), 16, 1024, 2).lo;
+      const uint32_t v_lo = desc_words(smem_addr(sKV), BN * 128, 1024, 2).lo;
+      auto opaque = [](uint32_t x) {
+        asm volatile("" : "+r"(x));
+        return x;
+      };
+      auto issue_s = [&](int w, int st) {
+        const DescWords q{opaque(q_lo + w * (TILE >> 4)), hi}, kd{opaque(k_lo + st * (TILE >> 4)), hi};
+        const uint32_t d = tbase + TR::S_COL + w * BN;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * (BM * 128) + (k & 3) * 32;
-          mma_bf16_ss(tbase + TR::S_COL + w * BN, desc_at(dQ, w * TILE + off), desc_at(dK, koff + off), idS, k > 0);
+          mma_bf16_ss(d, desc_at(q, off), desc_at(kd, off), idS, k > 0);
         }
         mma_commit(&s_full[w]);
       };
-      auto issue_pv = [&](int w, int i) {
-        const uint32_t voff = ((2 * i + 1) % STAGES) * TILE;
+      auto issue_pv = [&](int w, int st, bool first, bool last) {
+        const DescWords v{opaque(v_lo + st * (TILE >> 4)), hi};
+        const uint32_t d = tbase + TR::O_COL + w * D, a = tbase + TR::S_COL + w * BN;
 #pragma unroll
         for (int k = 0; k < BN / 16; ++k)
-          mma_bf16_ts(tbase + TR::O_COL + w * D, tbase + TR::S_COL + w * BN + k * 8, desc_at(dV, voff + k * 16 * 128),
-                      idO, i > 0 || k > 0);
-        if (i == n - 1) mma_commit(&o_done[w]);
+          mma_bf16_ts(d, a + k * 8, desc_at(v, k * 16 * 128), idO, !first || k > 0);
+        if (last) mma_commit(&o_done[w]);
       };
-      bool ok = mbar_wait(q_full, 0, s_abort) && wait_full(0);
+      bool ok = mbar_wait(q_full, 0, s_abort) && mbar_wait(&full[0], 0, s_abort);
       if (ok) {
         tc_fence_after();
         issue_s(0, 0);
         if (two) issue_s(1, 0);
         mma_commit(&empty[0]);
       }
+      int st = 1, round = 0;  // buffer of V_i and its use
       for (int i = 0; ok && i < n; ++i) {
-        if (!(ok = wait_full(2 * i + 1) && mbar_wait(&p_ready[0], i & 1, s_abort))) break;
+        const bool more = i + 1 < n;
+        if (!(ok = mbar_wait(&full[st], round & 1, s_abort) && mbar_wait(&p_ready[0], i & 1, s_abort))) break;
         tc_fence_after();
-        issue_pv(0, i);
-        if (i + 1 < n) {
-          if (!(ok = wait_full(2 * i + 2))) break;
-          issue_s(0, i + 1);
+        issue_pv(0, st, i == 0, !more);
+        const int v_st = st;
+        if (++st == STAGES) st = 0, ++round;
+        if (more) {
+          if (!(ok = mbar_wait(&full[st], round & 1, s_abort))) break;
+          tc_fence_after();
+          issue_s(0, st);
         }
         if (two) {
           if (!(ok = mbar_wait(&p_ready[1], i & 1, s_abort))) break;
           tc_fence_after();
-          issue_pv(1, i);
+          issue_pv(1, v_st, i == 0, !more);
         }
-        mma_commit(&empty[(2 * i + 1) % STAGES]);
-        if (i + 1 < n) {
-          if (two) issue_s(1, i + 1);
-          mma_commit(&empty[(2 * i + 2) % STAGES]);
+        mma_commit(&empty[v_st]);
+        if (more) {
+          if (two) issue_s(1, st);
+          mma_commit(&empty[st]);
+          if (++st == STAGES) st = 0, ++round;
         }
       }
       mma_commit(drain);
