@@ -449,6 +449,24 @@ def selftest_bounded_waits(stream=None) -> int:
 # Streams of single tokens: rotary positions, a paged pool of keys and values,
 # and attention of a ragged batch of sequences over it.
 # ---------------------------------------------------------------------------
+# These calls are made once per layer and token, so the marshalling is kept short:
+# one look at the current device, descriptors rebuilt only when a tensor changed.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device: int, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(device)
+
+
+def _on(t: torch.Tensor, device: int) -> int:
+    """_ptr on a device already looked up."""
+    if t.get_device() != device or not t.is_contiguous():
+        return _ptr(t)
+    return t.data_ptr()
+
+
 class TokenRope:
     """Rotary embedding of token positions (mirrors ll_token_rope_desc; ll_token_rope_init fills it).
 
@@ -488,12 +506,17 @@ class PagedKVCache:
             self.k_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
             self.v_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
         self.code = LL_FP8_E4M3 if dtype == "fp8" else LL_BF16
+        self._at, self._c = None, None
 
-    def to_c(self) -> PagedCacheC:
-        fp8 = self.k_scale is not None
-        return PagedCacheC(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr() if fp8 else None,
-                           self.v_scale.data_ptr() if fp8 else None, self.code, self.n_pages, self.page_size, self.H,
-                           self.D)
+    def to_c(self, device: Optional[int] = None) -> PagedCacheC:
+        """The descriptor; with a device, its tensors are checked to be there."""
+        tensors = (self.k, self.v) if self.k_scale is None else (self.k, self.v, self.k_scale, self.v_scale)
+        at = tuple([t.data_ptr() if device is None else _on(t, device) for t in tensors])
+        if at != self._at:
+            self._c = PagedCacheC(*(at if len(at) == 4 else at + (None, None)), self.code, self.n_pages, self.page_size,
+                                  self.H, self.D)
+            self._at = at
+        return self._c
 
 
 class TokenBatch:
@@ -514,10 +537,17 @@ class TokenBatch:
         _expect(kv_len, (B,), torch.int32, "kv_len")
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
         self.B, self.max_pages, self.max_q, self.max_kv = B, max_pages, int(max_q), int(max_kv)
+        self._key, self._c = None, None
 
-    def to_c(self, total_q: int) -> TokenBatchC:
-        return TokenBatchC(_ptr(self.q_start), _ptr(self.kv_len), _ptr(self.page_table), self.B, self.max_pages,
-                           total_q, self.max_q, self.max_kv)
+    def to_c(self, total_q: int, device: int) -> TokenBatchC:
+        key = (_on(self.q_start, device), _on(self.kv_len, device), _on(self.page_table, device), self.B,
+               self.max_pages, total_q, self.max_q, self.max_kv)
+        if key != self._key:
+            # a new structure, not a changed one: another thread may be in a call with the old
+            c = TokenBatchC(*key)
+            self._key, self._c = key, c
+            return c
+        return self._c
 
 
 class Scores:
@@ -543,70 +573,77 @@ class Scores:
         return c
 
 
-def _rows(t: torch.Tensor, what: str, H: Optional[int] = None, D: Optional[int] = None):
+def _rows(t: torch.Tensor, what: str, device: int, H: Optional[int] = None, D: Optional[int] = None):
     """(address, row stride in elements) of a CUDA tensor [T, H, D] whose heads lie
     together; rows may be further apart (a slice of a fused projection)."""
-    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (D is not None and t.shape[2] != D):
+    if t.dim() != 3:
         raise ValueError(f"{what} must be [rows, {H or 'heads'}, {D or 'D'}], got shape {tuple(t.shape)}")
     T, h, d = t.shape
+    if (H is not None and h != H) or (D is not None and d != D):
+        raise ValueError(f"{what} must be [rows, {H or 'heads'}, {D or 'D'}], got shape {tuple(t.shape)}")
     sr, sh, sd = t.stride()
     if T <= 1:
         sr = h * d
-    if t.numel() > 0 and ((sd != 1 and d > 1) or (sh != d and h > 1)):
+    if T > 0 and ((sd != 1 and d > 1) or (sh != d and h > 1)):
         raise ValueError(f"the heads of a row of {what} must be contiguous, got strides {t.stride()}")
-    if not t.is_cuda:
-        raise ValueError(f"tensors must be CUDA tensors, got one on {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current CUDA device (cuda:{torch.cuda.current_device()}), "
-                         f"got one on {t.device}")
+    if t.get_device() != device:
+        if not t.is_cuda:
+            raise ValueError(f"tensors must be CUDA tensors, got one on {t.device}")
+        raise ValueError(f"tensors must be on the current CUDA device (cuda:{device}), got one on {t.device}")
     return t.data_ptr(), sr
+
+
+def _device(t: torch.Tensor) -> int:
+    """The current CUDA device, where the call's tensors have to be (none for a host
+    tensor, which _rows refuses)."""
+    return torch.cuda.current_device() if t.is_cuda else -2
 
 
 def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """A new tensor that belongs to the stream the kernels run on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def token_rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: TokenRope, transpose: bool = False,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotate x [T, H, D] (bf16 or f32) at its tokens' positions (int32 [T]);
     transpose=True applies the transposed rotation: the gradient. out may be x."""
-    xp, xs = _rows(x, "x")
+    dev = _device(x)
+    xp, xs = _rows(x, "x", dev)
     T, H, D = x.shape
     _expect(positions, (T,), torch.int32, "positions")
     if out is None:
         out = _empty(x.shape, x.dtype, x, stream)
-    elif out.dtype != x.dtype or out.shape != x.shape:
-        raise ValueError(f"out must be a {x.dtype} tensor of shape {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
-    op, os_ = _rows(out, "out")
+        op, os_ = out.data_ptr(), H * D
+    else:
+        if out.dtype != x.dtype or out.shape != x.shape:
+            raise ValueError(f"out must be a {x.dtype} tensor of shape {tuple(x.shape)}, "
+                             f"got {out.dtype} {tuple(out.shape)}")
+        op, os_ = _rows(out, "out", dev)
     if T == 0:
         return out
-    _check(lib().ll_token_rope_apply(xp, xs, op, os_, _dtype_code(x.dtype), _ptr(positions), T, H, D, rope.to_c(),
-                                     int(transpose), _stream(stream)))
+    _check(lib().ll_token_rope_apply(xp, xs, op, os_, _dtype_code(x.dtype), _on(positions, dev), T, H, D, rope._c,
+                                     1 if transpose else 0, _stream_of(dev, stream)))
     return out
-
-
-def _pool_c(cache: PagedKVCache) -> PagedCacheC:
-    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
-        _ptr(t)
-    return cache.to_c()
 
 
 def paged_append(cache: PagedKVCache, batch: TokenBatch, k: torch.Tensor, v: torch.Tensor,
                  rope: Optional[TokenRope] = None, stream=None) -> None:
     """Write the batch's new tokens, k and v [total_q, H, D] bf16, into their
     pages, K rotated at its positions (ll_paged_append). Rows may be strided."""
-    kp, ks = _rows(k, "k", cache.H, cache.D)
-    vp, vs = _rows(v, "v", cache.H, cache.D)
-    if k.shape != v.shape or k.dtype != v.dtype:
+    dev = _device(k)
+    kp, ks = _rows(k, "k", dev, cache.H, cache.D)
+    vp, vs = _rows(v, "v", dev, cache.H, cache.D)
+    T = k.shape[0]
+    if v.shape[0] != T or k.dtype != v.dtype:
         raise ValueError("k and v must have one shape and dtype")
-    if k.shape[0] == 0:
+    if T == 0:
         return
-    _check(lib().ll_paged_append(_pool_c(cache), batch.to_c(k.shape[0]), kp, ks, vp, vs, _dtype_code(k.dtype),
-                                 None if rope is None else rope.to_c(), _stream(stream)))
+    _check(lib().ll_paged_append(cache.to_c(dev), batch.to_c(T, dev), kp, ks, vp, vs, _dtype_code(k.dtype),
+                                 None if rope is None else rope._c, _stream_of(dev, stream)))
 
 
 def paged_attention_workspace_bytes(cache: PagedKVCache, batch: TokenBatch, total_q: int, Hq: int) -> int:
@@ -622,21 +659,31 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: TokenBatch, rop
     strided; rotated here when rope is given) over the pool, which already holds
     their keys and values (ll_paged_attention). Rows of no sequence are not
     written: they keep what `out` held."""
-    T, Hq = q.shape[0], q.shape[1]
-    qp, qs = _rows(q, "q", None, cache.D)
+    dev = _device(q)
+    qp, qs = _rows(q, "q", dev, None, cache.D)
+    T, Hq, D = q.shape
     if out is None:
-        out = _empty((T, Hq, cache.D), q.dtype, q, stream)
-    _expect(out, (T, Hq, cache.D), q.dtype, "out")
-    _expect(lse, (T, Hq), torch.float32, "lse")
+        out = _empty((T, Hq, D), q.dtype, q, stream)
+        op = out.data_ptr()
+    else:
+        _expect(out, (T, Hq, D), q.dtype, "out")
+        op = _on(out, dev)
+    lp = None
+    if lse is not None:
+        _expect(lse, (T, Hq), torch.float32, "lse")
+        lp = _on(lse, dev)
     if T == 0:
         return out
-    L, pool, tokens = lib(), _pool_c(cache), batch.to_c(T)
+    L, pool, tokens = lib(), cache.to_c(dev), batch.to_c(T, dev)
+    wp, ws_bytes = None, 0
     if workspace is None:
-        n = L.ll_paged_attention_workspace_bytes(pool, tokens, Hq)
-        if n:
-            workspace = _empty((n,), torch.uint8, q, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(L.ll_paged_attention(qp, qs, _dtype_code(q.dtype), Hq, pool, tokens, None if rope is None else rope.to_c(),
-                                None if scores is None else scores.to_c(batch.B, Hq), _ptr(out), _ptr(lse),
-                                _ptr(workspace), ws_bytes, _stream(stream)))
+        ws_bytes = L.ll_paged_attention_workspace_bytes(pool, tokens, Hq)
+        if ws_bytes:
+            workspace = _empty((ws_bytes,), torch.uint8, q, stream)
+            wp = workspace.data_ptr()
+    else:
+        wp, ws_bytes = _on(workspace, dev), workspace.numel() * workspace.element_size()
+    _check(L.ll_paged_attention(qp, qs, _dtype_code(q.dtype), Hq, pool, tokens, None if rope is None else rope._c,
+                                None if scores is None else scores.to_c(batch.B, Hq), op, lp, wp, ws_bytes,
+                                _stream_of(dev, stream)))
     return out

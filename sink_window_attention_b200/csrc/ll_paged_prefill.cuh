@@ -22,6 +22,8 @@
 // for the powers of two that the append writes) is multiplied into V's fp16.
 #pragma once
 
+#include <type_traits>
+
 #include "ll_paged_attention.cuh"
 
 namespace ll {
@@ -72,6 +74,24 @@ __device__ __forceinline__ float2 turn_fast(const TokenRope& r, long long pos, i
   if ((quarter + 1) & 2) x = -x;
   if (quarter & 2) y = -y;
   return make_float2(x * r.amp, y * r.amp);
+}
+
+// mbar_wait for the loaders, who are buffers ahead: they sleep between polls, which
+// would take issue slots from the softmax.
+__device__ __forceinline__ bool mbar_wait_sleeping(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_addr(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(a, parity)) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      atomicOr(&g_error_word, kErrWaitTimeout);
+      *abort = 1;
+      return false;
+    }
+    __nanosleep(100);
+  }
+  return true;
 }
 
 template <class TR, bool MODS>
@@ -170,7 +190,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       mbar_arrive(&full[st]);
     };
     auto wait_empty = [&](int st, int round) {
-      if (ok) ok = mbar_wait(&empty[st], (round & 1) ^ 1, s_abort);
+      if (ok) ok = mbar_wait_sleeping(&empty[st], (round & 1) ^ 1, s_abort);
       ok = __all_sync(0xffffffffu, ok);
     };
     auto put_meta = [&](int i) {
@@ -206,17 +226,22 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
           if (!ok) break;
           const uint8_t* src = static_cast<const uint8_t*>(kv ? p.pool.v : p.pool.k) + lane_off;
           const uint32_t dst = dst0 + st * TILE;
+          // a run's rows are whole 8-row swizzle atoms apart, so the swizzle is r's
+          auto copy = [&](auto all) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const int at = __shfl_sync(0xffffffffu, run, g);
-            const uint8_t* from = src + static_cast<size_t>(at < 0 ? 0 : at) * (16 * D * 2);
+            for (int g = 0; g < 8; ++g) {
+              const int at = __shfl_sync(0xffffffffu, run, g);
+              const uint8_t* from = src + static_cast<size_t>(at < 0 ? 0 : at) * (16 * D * 2);
 #pragma unroll
-            for (int k = 0; k < PER_RUN; ++k) {
-              const int row = g * 16 + k * RPS;  // + r; whole 8-row swizzle atoms, so the swizzle is r's
-              const bool valid = at >= 0 && (whole || kr.some_row_sees(key0 + row + r));
-              cp_async16(dst + row * 128, from + k * (RPS * D * 2), valid);
+              for (int k = 0; k < PER_RUN; ++k) {
+                const int row = g * 16 + k * RPS;  // + r
+                const bool valid = at >= 0 && (all || kr.some_row_sees(key0 + row + r));
+                cp_async16(dst + row * 128, from + k * (RPS * D * 2), valid);
+              }
             }
-          }
+          };
+          if (whole) copy(std::true_type{});
+          else copy(std::false_type{});
           cp_async_commit();
           if (kv == 0) put_meta(i);
           if (++behind > AHEAD) {
@@ -252,13 +277,14 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       uint4 buf[2][STEPS];
       auto load_step = [&](const void* pool, int run, int key0, bool whole, int k) -> uint4 {
         const int at = __shfl_sync(0xffffffffu, run, (r + k * RPS) >> 4);
+        bool valid = at >= 0;
+        if (!whole) valid = valid && kr.some_row_sees(key0 + r + k * RPS);
+        const uint8_t* from = static_cast<const uint8_t*>(pool) + static_cast<size_t>(at) * (16 * D) + lane_off;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (at >= 0 && (whole || kr.some_row_sees(key0 + r + k * RPS))) {
-          const uint8_t* from = static_cast<const uint8_t*>(pool) + static_cast<size_t>(at) * (16 * D) + lane_off;
+        if (valid)
           asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                        : "l"(from));
-        }
         return u;
       };
       if (n > 0) {
