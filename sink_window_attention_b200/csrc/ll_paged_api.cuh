@@ -163,9 +163,9 @@ size_t paged_workspace(const AttnPlan& a, const ll_token_batch* t, int Hq, int D
          align256(static_cast<size_t>(t->total_q) * Hq * a.nsplit * sizeof(float2));
 }
 
-template <class TR>
+template <class TR, bool MODS>
 ll_status launch_paged_decode(const ll::PagedAttnParams& p, cudaStream_t s) {
-  auto kern = ll::paged_decode_kernel<TR>;
+  auto kern = ll::paged_decode_kernel<TR, MODS>;
   static std::atomic<unsigned long long> done{0};
   ll_status st = allow_smem(kern, TR::SMEM, done);
   if (st != LL_OK) return st;
@@ -185,9 +185,13 @@ ll_status launch_paged_prefill(const ll::PagedAttnParams& p, cudaStream_t s) {
 
 template <int D, bool E4M3>
 ll_status launch_paged(const AttnPlan& plan, const ll::PagedAttnParams& p, cudaStream_t s) {
-  if (!plan.tiles) return launch_paged_decode<ll::DecodeTraits<D, E4M3>>(p, s);
+  const bool mods = p.sc.cap2 > 0.f || p.sc.biased;  // scores are more than a scaled product
+  if (!plan.tiles) {
+    using TR = ll::DecodeTraits<D, E4M3>;
+    return mods ? launch_paged_decode<TR, true>(p, s) : launch_paged_decode<TR, false>(p, s);
+  }
   using TR = ll::PrefillTraits<D, E4M3>;
-  return p.sc.cap2 > 0.f || p.sc.biased ? launch_paged_prefill<TR, true>(p, s) : launch_paged_prefill<TR, false>(p, s);
+  return mods ? launch_paged_prefill<TR, true>(p, s) : launch_paged_prefill<TR, false>(p, s);
 }
 
 // The join starts while the pieces' kernel drains and waits for its end on the

@@ -6,6 +6,8 @@
 //   x = scale q.k, soft-capped, biased by distance; masked keys have no x.
 #pragma once
 
+#include <type_traits>
+
 #include "ll_tokens.cuh"
 
 namespace ll {
@@ -151,10 +153,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two E4M3 codes as two halves (exact).
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four E4M3 codes as two pairs of halves (exact).
+__device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 // ---------------------------------------------------------------------------
@@ -197,13 +203,26 @@ struct DecodeTraits {
   static_assert(NW * 16 * D * 4 <= RING, "the warps' O must fit the ring");
 };
 
+// O's columns of four neighbouring d: keys 2t, 2t+1 (a, b) and 2t+8, 2t+9 (c, d), one
+// word of four codes each.
+__device__ __forceinline__ void pv_e4m3(float (*o)[4], const uint32_t (&pa)[4], uint32_t a, uint32_t b, uint32_t c,
+                                        uint32_t d) {
+  uint32_t x[4], y[4];
+  e4m3x4_f16(__byte_perm(a, b, 0x5140), x[0], x[1]);
+  e4m3x4_f16(__byte_perm(a, b, 0x7362), x[2], x[3]);
+  e4m3x4_f16(__byte_perm(c, d, 0x5140), y[0], y[1]);
+  e4m3x4_f16(__byte_perm(c, d, 0x7362), y[2], y[3]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) mma16816<true>(o[e], pa, x[e], y[e]);
+}
+
 template <int CH>
 __device__ __forceinline__ int swz(int row, int c) {
   if constexpr (CH == 4) return c ^ ((row >> 1) & 3);
   return c ^ ((((row ^ (row >> 2)) & 1) << 2) | (row & 2));
 }
 
-template <class TR>
+template <class TR, bool MODS>
 __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(const PagedAttnParams p) {
   constexpr int D = TR::D, CH = TR::CH, NW = TR::NW, STAGES = TR::STAGES, TILE = TR::TILE;
   constexpr bool E4M3 = TR::E4M3;
@@ -235,8 +254,6 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   // ---- the ring
   const uint32_t ring = smem_addr(s_ring) + warp * (STAGES * 2 * TILE);
   const uint32_t meta = smem_addr(s_meta) + warp * (STAGES * 16);
-  const uint8_t* kp = static_cast<const uint8_t*>(p.pool.k);
-  const uint8_t* vp = static_cast<const uint8_t*>(p.pool.v);
   int my_page = -1;
   auto issue = [&](int k) {
     if (k < n_my) {
@@ -248,16 +265,24 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
       const int key0 = kr.tile(t_beg + k * NW) * 16;
       const int st = k % STAGES;
       const size_t head = static_cast<size_t>(page < 0 ? 0 : page) * p.pool.H + hkv;
-      const size_t src = (head * ps + (key0 & (ps - 1))) * TR::ROWB;
+      const size_t src = (head * ps + (key0 & (ps - 1))) * TR::ROWB + lane * 16;
+      const uint8_t* kfrom = static_cast<const uint8_t*>(p.pool.k) + src;
+      const uint8_t* vfrom = static_cast<const uint8_t*>(p.pool.v) + src;
       const uint32_t dst = ring + st * (2 * TILE);
+      // every key is seen by some row, or each is looked at
+      const bool whole = key0 + 16 <= kr.always || (key0 >= kr.lo && key0 + 16 <= kr.upper);
+      auto copy = [&](auto all) {
 #pragma unroll
-      for (int i = 0; i < TILE / 512; ++i) {
-        const int c = lane + 32 * i, row = c / CH, ch = c % CH;
-        const bool ok = page >= 0 && kr.some_row_sees(key0 + row);
-        const uint32_t to = dst + row * TR::ROWB + (swz<CH>(row, ch) << 4);
-        cp_async16(to, kp + src + c * 16, ok);
-        cp_async16(to + TILE, vp + src + c * 16, ok);
-      }
+        for (int i = 0; i < TILE / 512; ++i) {
+          const int c = lane + 32 * i, row = c / CH, ch = c % CH;
+          const bool ok = page >= 0 && (all || kr.some_row_sees(key0 + row));
+          const uint32_t to = dst + row * TR::ROWB + (swz<CH>(row, ch) << 4);
+          cp_async16(to, kfrom + i * 512, ok);
+          cp_async16(to + TILE, vfrom + i * 512, ok);
+        }
+      };
+      if (whole) copy(std::true_type{});
+      else copy(std::false_type{});
       if constexpr (E4M3) {
         if (lane < 2) cp_async4(meta + st * 16 + lane * 4, (lane ? p.pool.v_scale : p.pool.k_scale) + head, page >= 0);
       }
@@ -334,7 +359,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   const int prow[2] = {r0 + g, r0 + g + 8};
   const long long pos[2] = {s.first_pos + prow[0] / p.group, s.first_pos + prow[1] / p.group};
   float slope[2] = {0.f, 0.f};
-  if (p.sc.biased) {
+  if (MODS && p.sc.biased) {
     slope[0] = p.sc.slope2[hkv * p.group + prow[0] % p.group];
     slope[1] = p.sc.slope2[hkv * p.group + prow[1] % p.group];
   }
@@ -371,7 +396,11 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         if constexpr (E4M3) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma16816<true>(sx[n], aq[i * 4 + e], e4m3x2_f16(w[e]), e4m3x2_f16(w[e] >> 16));
+          for (int e = 0; e < 4; ++e) {
+            uint32_t b0, b1;
+            e4m3x4_f16(w[e], b0, b1);
+            mma16816<true>(sx[n], aq[i * 4 + e], b0, b1);
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 2; ++e) mma16816<false>(sx[n], aq[i * 2 + e], w[2 * e], w[2 * e + 1]);
@@ -384,8 +413,11 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[r][e] = score2(p.sc, sx[e >> 1][2 * r + (e & 1)], fac[r] * ks);
-    if (p.sc.biased) {
+      for (int e = 0; e < 4; ++e) {
+        const float y = sx[e >> 1][2 * r + (e & 1)], f = fac[r] * ks;
+        x[r][e] = MODS ? score2(p.sc, y, f) : y * f;
+      }
+    if (MODS && p.sc.biased) {
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -455,12 +487,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t a01 = __byte_perm(w[0][i], w[1][i], 0x5140), a23 = __byte_perm(w[0][i], w[1][i], 0x7362);
-        const uint32_t c01 = __byte_perm(w[2][i], w[3][i], 0x5140), c23 = __byte_perm(w[2][i], w[3][i], 0x7362);
-        mma16816<true>(o[4 * i], pa, e4m3x2_f16(a01), e4m3x2_f16(c01));
-        mma16816<true>(o[4 * i + 1], pa, e4m3x2_f16(a01 >> 16), e4m3x2_f16(c01 >> 16));
-        mma16816<true>(o[4 * i + 2], pa, e4m3x2_f16(a23), e4m3x2_f16(c23));
-        mma16816<true>(o[4 * i + 3], pa, e4m3x2_f16(a23 >> 16), e4m3x2_f16(c23 >> 16));
+        pv_e4m3(&o[4 * i], pa, w[0][i], w[1][i], w[2][i], w[3][i]);
       }
     } else {
 #pragma unroll
@@ -478,12 +505,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (E4M3) {
-            const uint32_t a01 = __byte_perm(w[0][e], w[1][e], 0x5140), a23 = __byte_perm(w[0][e], w[1][e], 0x7362);
-            const uint32_t c01 = __byte_perm(w[2][e], w[3][e], 0x5140), c23 = __byte_perm(w[2][e], w[3][e], 0x7362);
-            mma16816<true>(o[4 * e], pa, e4m3x2_f16(a01), e4m3x2_f16(c01));
-            mma16816<true>(o[4 * e + 1], pa, e4m3x2_f16(a01 >> 16), e4m3x2_f16(c01 >> 16));
-            mma16816<true>(o[4 * e + 2], pa, e4m3x2_f16(a23), e4m3x2_f16(c23));
-            mma16816<true>(o[4 * e + 3], pa, e4m3x2_f16(a23 >> 16), e4m3x2_f16(c23 >> 16));
+            pv_e4m3(&o[4 * e], pa, w[0][e], w[1][e], w[2][e], w[3][e]);
           } else {
             mma16816<false>(o[i * 8 + 2 * e], pa, __byte_perm(w[0][e], w[1][e], 0x5410),
                             __byte_perm(w[2][e], w[3][e], 0x5410));

@@ -314,10 +314,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
             const uint32_t w[4] = {buf[kv][k].x, buf[kv][k].y, buf[kv][k].z, buf[kv][k].w};
             uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[2 * e] = e4m3x2_f16(w[e]);
-              h[2 * e + 1] = e4m3x2_f16(w[e] >> 16);
-            }
+            for (int e = 0; e < 4; ++e) e4m3x4_f16(w[e], h[2 * e], h[2 * e + 1]);
             if (kv && !plain) {  // a scale that is no power of two
               const __half2 f2 = __float2half2_rn(__shfl_sync(0xffffffffu, mant, (r + k * RPS) >> 4));
 #pragma unroll
