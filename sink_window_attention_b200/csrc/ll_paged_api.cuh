@@ -124,7 +124,7 @@ AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq
   const long long cap = static_cast<long long>(t->max_pages) * c->page_size;
   const long long max_kv = t->max_kv < cap ? t->max_kv : cap;
   a.tiles = max_q * group > kDecodeRows;
-  a.row_tile = a.tiles ? 256 : 16;
+  a.row_tile = a.tiles ? 256 : (max_q * group <= 8 ? 8 : 16);
   a.key_tile = a.tiles ? 128 : 16;
   a.row_tiles = static_cast<int>((max_q * group + a.row_tile - 1) / a.row_tile);
   // at most (window and prefix only shorten a range)
@@ -187,7 +187,11 @@ template <int D, bool E4M3>
 ll_status launch_paged(const AttnPlan& plan, const ll::PagedAttnParams& p, cudaStream_t s) {
   const bool mods = p.sc.cap2 > 0.f || p.sc.biased;  // scores are more than a scaled product
   if (!plan.tiles) {
-    using TR = ll::DecodeTraits<D, E4M3>;
+    if (plan.row_tile == 8) {
+      using TR = ll::DecodeTraits<D, E4M3, 8>;
+      return mods ? launch_paged_decode<TR, true>(p, s) : launch_paged_decode<TR, false>(p, s);
+    }
+    using TR = ll::DecodeTraits<D, E4M3, 16>;
     return mods ? launch_paged_decode<TR, true>(p, s) : launch_paged_decode<TR, false>(p, s);
   }
   using TR = ll::PrefillTraits<D, E4M3>;

@@ -138,19 +138,27 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8)
 template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
   if constexpr (F16)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values, two neighbouring columns per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Four E4M3 codes as two pairs of halves (exact).
@@ -164,33 +172,36 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t& lo, uint32_t
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (decode). One block: 16 rows of a sequence and K/V head against a
+// Few rows (decode). One block: 8 or 16 rows of a sequence and K/V head against a
 // piece of its keys; the block's warps take 16-key tiles in turn, each with a
 // ring of its own in shared memory that cp.async keeps full, and meet once at
-// the end. What bounds it is the pool's bytes, so nothing but loads in flight
-// matters: 4 warps x (STAGES - 1) tiles of K and V per block, several blocks
-// per SM. The matrix instruction is the warp-level one (16 x 8 x 16): a
-// tensor-memory tile has 128 rows, of which a decode step fills 1 to 16.
+// the end. What bounds it is the pool's bytes: 4 warps x (STAGES - 1) tiles of K
+// and V in flight per block, several blocks per SM, and few instructions per tile.
+// The matrix instruction is the warp-level one (16 x 8 x 16): a tensor-memory tile
+// has 128 rows, of which a decode step fills 1 to 16.
 //
-// The reduction index of an MMA may be permuted when both operands are, so
-// neither K nor V needs a transposing load:
-//  * S = Q K^T: lane (g, t) holds key g and takes whole 16-byte chunks t, t + 4,
-//    .. of its row; Q's fragments use the same order of d.
-//  * O = P V: the lane's columns of S are keys 2t, 2t+1, 2t+8, 2t+9, so P is an
-//    A operand as it stands; the lane reads those four rows of V at chunk g
-//    (+ 8), and byte permutes pair two keys at the same d.
+// Keys (and then d) are the MMA's 16 rows, the query rows its 8 columns, so 8 query
+// rows waste nothing: S^T = K Q^T, then O^T = V^T P^T. The reduction index of an MMA
+// may be permuted when both operands are, so neither K nor V needs a transposing load:
+//  * S^T: lane (g, t) holds keys g and g + 8 and takes whole 16-byte chunks t, t + 4,
+//    .. of their rows; Q's fragments use the same order of d.
+//  * O^T: P leaves S^T with keys along lanes g and is turned by two 8 x 8 transposes;
+//    the lane reads the V rows of keys 2t, 2t+1, 2t+8, 2t+9 at chunk g (+ 8), and
+//    byte permutes pair two keys at the same d.
 // ---------------------------------------------------------------------------
-template <int D_, bool E4M3_>
+template <int D_, bool E4M3_, int ROWS_>
 struct DecodeTraits {
   static constexpr int D = D_;
   static constexpr bool E4M3 = E4M3_;
+  static constexpr int ROWS = ROWS_;        // 8 or 16
+  static constexpr int NR = ROWS / 8;       // MMAs side by side over the rows
   static constexpr int ES = E4M3 ? 1 : 2;
   static constexpr int ROWB = D * ES;
   static constexpr int CH = ROWB / 16;      // chunks per row
-  static constexpr int KC = CH / 4;         // chunks of K per lane
+  static constexpr int KC = CH / 4;         // chunks of a K row per lane
   static constexpr int EPC = 16 / ES;       // elements per chunk
   static constexpr int KS = D / 16;         // MMAs over d
-  static constexpr int NT = D / 8;          // MMAs over O's columns
+  static constexpr int MT = D / 16;         // MMAs over O^T's rows
   static constexpr int TILE = 16 * ROWB;
   static constexpr int NW = 4;
   static constexpr int THREADS = NW * 32;
@@ -199,22 +210,9 @@ struct DecodeTraits {
   static constexpr int QP = D + 8;          // 16-bit elements between rows of Q
   static constexpr int BLOCKS = ROWB >= 256 ? 2 : 3;  // per SM, by shared memory
   static constexpr int META = NW * STAGES * 16;
-  static constexpr int SMEM = RING + META + 16 * QP * 2 + 16 * 4 + 2 * NW * 16 * 4;
-  static_assert(NW * 16 * D * 4 <= RING, "the warps' O must fit the ring");
+  static constexpr int SMEM = RING + META + ROWS * QP * 2 + ROWS * 4 + 2 * NW * ROWS * 4;
+  static_assert(NW * ROWS * D * 4 <= RING, "the warps' O must fit the ring");
 };
-
-// O's columns of four neighbouring d: keys 2t, 2t+1 (a, b) and 2t+8, 2t+9 (c, d), one
-// word of four codes each.
-__device__ __forceinline__ void pv_e4m3(float (*o)[4], const uint32_t (&pa)[4], uint32_t a, uint32_t b, uint32_t c,
-                                        uint32_t d) {
-  uint32_t x[4], y[4];
-  e4m3x4_f16(__byte_perm(a, b, 0x5140), x[0], x[1]);
-  e4m3x4_f16(__byte_perm(a, b, 0x7362), x[2], x[3]);
-  e4m3x4_f16(__byte_perm(c, d, 0x5140), y[0], y[1]);
-  e4m3x4_f16(__byte_perm(c, d, 0x7362), y[2], y[3]);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) mma16816<true>(o[e], pa, x[e], y[e]);
-}
 
 template <int CH>
 __device__ __forceinline__ int swz(int row, int c) {
@@ -225,21 +223,22 @@ __device__ __forceinline__ int swz(int row, int c) {
 template <class TR, bool MODS>
 __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(const PagedAttnParams p) {
   constexpr int D = TR::D, CH = TR::CH, NW = TR::NW, STAGES = TR::STAGES, TILE = TR::TILE;
+  constexpr int ROWS = TR::ROWS, NR = TR::NR, MT = TR::MT;
   constexpr bool E4M3 = TR::E4M3;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* s_ring = smem;
   float* s_meta = reinterpret_cast<float*>(smem + TR::RING);  // [NW][STAGES][4]: K scale, V scale, page mapped
-  uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + TR::RING + TR::META);  // [16][QP]
-  float* s_qf = reinterpret_cast<float*>(s_q + 16 * TR::QP);                // [16]
-  float* s_m = s_qf + 16;                                                   // [NW][16]
-  float* s_l = s_m + NW * 16;
+  uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + TR::RING + TR::META);  // [ROWS][QP]
+  float* s_qf = reinterpret_cast<float*>(s_q + ROWS * TR::QP);              // [ROWS]
+  float* s_m = s_qf + ROWS;                                                 // [NW][ROWS]
+  float* s_l = s_m + NW * ROWS;
 
   asm volatile("griddepcontrol.launch_dependents;");
   const int rt = blockIdx.x % p.row_tiles, split = blockIdx.x / p.row_tiles;
   const int hkv = blockIdx.y, b = blockIdx.z;
   const int ps = p.pool.page_size;
   const SeqView s = seq_view(p.batch, b, ps);
-  const int rows = s.nq * p.group, r0 = rt * 16;
+  const int rows = s.nq * p.group, r0 = rt * ROWS;
   if (r0 >= rows) return;
   long long p_lo, p_hi;
   unit_positions(p, s, r0, p_lo, p_hi);
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   for (int k = 0; k < STAGES - 1; ++k) issue(k);
 
   // ---- Q: rotated in fp32, rounded to the MMA's type
-  for (int i = threadIdx.x; i < 16 * (D / 16); i += TR::THREADS) {
+  for (int i = threadIdx.x; i < ROWS * (D / 16); i += TR::THREADS) {
     const int r = i / (D / 16), c = i % (D / 16);
     const int row = r0 + r, tok = row / p.group, h = hkv * p.group + row % p.group;
     int lo, hi;
@@ -343,38 +342,44 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   __syncthreads();
 
   const int g = lane >> 2, t = lane & 3;
-  uint32_t aq[TR::KS][4];
+  uint32_t bq[NR][TR::KS][2];
+  // this lane's query rows: 2t + q + 8r at [2r + q]
+  float fac[2 * NR], slope[2 * NR];
+  int pos[2 * NR];
 #pragma unroll
-  for (int j = 0; j < TR::KS; ++j) {
-    constexpr int U = TR::EPC / 4;  // MMAs per chunk
-    const int d = (t + 4 * (j / U)) * TR::EPC + 4 * (j % U);
-    const uint2 u0 = *reinterpret_cast<const uint2*>(s_q + g * TR::QP + d);
-    const uint2 u1 = *reinterpret_cast<const uint2*>(s_q + (g + 8) * TR::QP + d);
-    aq[j][0] = u0.x;
-    aq[j][1] = u1.x;
-    aq[j][2] = u0.y;
-    aq[j][3] = u1.y;
-  }
-  const float fac[2] = {s_qf[g] * p.sc.pre, s_qf[g + 8] * p.sc.pre};
-  const int prow[2] = {r0 + g, r0 + g + 8};
-  const long long pos[2] = {s.first_pos + prow[0] / p.group, s.first_pos + prow[1] / p.group};
-  float slope[2] = {0.f, 0.f};
-  if (MODS && p.sc.biased) {
-    slope[0] = p.sc.slope2[hkv * p.group + prow[0] % p.group];
-    slope[1] = p.sc.slope2[hkv * p.group + prow[1] % p.group];
+  for (int r = 0; r < NR; ++r) {
+#pragma unroll
+    for (int j = 0; j < TR::KS; ++j) {
+      constexpr int U = TR::EPC / 4;  // MMAs per chunk
+      const int d = (t + 4 * (j / U)) * TR::EPC + 4 * (j % U);
+      const uint2 u = *reinterpret_cast<const uint2*>(s_q + (g + 8 * r) * TR::QP + d);
+      bq[r][j][0] = u.x;
+      bq[r][j][1] = u.y;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int row = 2 * t + q + 8 * r;
+      fac[2 * r + q] = s_qf[row] * p.sc.pre;
+      pos[2 * r + q] = static_cast<int>(max(s.first_pos + (r0 + row) / p.group, -(1ll << 30)));
+      slope[2 * r + q] = MODS && p.sc.biased ? p.sc.slope2[hkv * p.group + (r0 + row) % p.group] : 0.f;
+    }
   }
 
-  float o[TR::NT][4];
+  float o[NR][MT][4];
 #pragma unroll
-  for (int n = 0; n < TR::NT; ++n)
+  for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[r][n][e] = 0.f;
   // m: reference of the row's exponents (a running max, raised only when it is
   // exceeded by 2^8: sums and O are rescaled rarely); l: this lane's share of the
   // sum. Over an 8-bit pool V's codes enter the MMA as they are and their scale
   // goes with P = p vs, so the reference is the max of x + log2(vs): P then stays
   // inside fp16 whatever the pages' scales are, p itself is fp32.
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2 * NR], l[2 * NR];
+#pragma unroll
+  for (int q = 0; q < 2 * NR; ++q) m[q] = -INFINITY, l[q] = 0.f;
 
   for (int k = 0; k < n_my; ++k) {
     cp_async_wait<STAGES - 2>();
@@ -384,135 +389,139 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     const uint8_t* sv = sk + TILE;
     const float4 mt = *reinterpret_cast<const float4*>(s_meta + (warp * STAGES + st) * 4);
     const int key0 = kr.tile(t_beg + k * NW) * 16;
-    float sx[2][4];
+    // S^T: [key g: row 2t, 2t+1][key g + 8: row 2t, 2t+1]
+    float sx[NR][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sx[n][e] = 0.f;
-      const int row = g + 8 * n;
+      for (int e = 0; e < 4; ++e) sx[r][e] = 0.f;
 #pragma unroll
-      for (int i = 0; i < TR::KC; ++i) {
-        const uint4 u = *reinterpret_cast<const uint4*>(sk + row * TR::ROWB + (swz<CH>(row, t + 4 * i) << 4));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t b0, b1;
-            e4m3x4_f16(w[e], b0, b1);
-            mma16816<true>(sx[n], aq[i * 4 + e], b0, b1);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) mma16816<false>(sx[n], aq[i * 2 + e], w[2 * e], w[2 * e + 1]);
-        }
-      }
-    }
-    // scores in log2 units: x[row][key], keys 2t, 2t+1, 2t+8, 2t+9 of the tile
-    float x[2][4];
-    const float ks = E4M3 ? mt.x : 1.f;
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float y = sx[e >> 1][2 * r + (e & 1)], f = fac[r] * ks;
-        x[r][e] = MODS ? score2(p.sc, y, f) : y * f;
-      }
-    if (MODS && p.sc.biased) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
+    for (int i = 0; i < TR::KC; ++i) {
+      const int ch = swz<CH>(g, t + 4 * i) << 4;  // g + 8 is swizzled like g
+      const uint4 u = *reinterpret_cast<const uint4*>(sk + g * TR::ROWB + ch);
+      const uint4 w = *reinterpret_cast<const uint4*>(sk + (g + 8) * TR::ROWB + ch);
+      const uint32_t ua[4] = {u.x, u.y, u.z, u.w}, wa[4] = {w.x, w.y, w.z, w.w};
+      if constexpr (E4M3) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = key0 + 2 * t + (e & 1) + 8 * (e >> 1);
-          x[r][e] -= slope[r] * fabsf(static_cast<float>(pos[r] - j));
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_f16(ua[e], a0, a2);
+          e4m3x4_f16(wa[e], a1, a3);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) mma16816<true>(sx[r], a0, a1, a2, a3, bq[r][i * 4 + e][0], bq[r][i * 4 + e][1]);
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            mma16816<false>(sx[r], ua[2 * e], wa[2 * e], ua[2 * e + 1], wa[2 * e + 1], bq[r][i * 2 + e][0],
+                            bq[r][i * 2 + e][1]);
+      }
     }
+    // scores in log2 units
+    const float ks = E4M3 ? mt.x : 1.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = fac[2 * r + (e & 1)] * ks;
+        sx[r][e] = MODS ? score2(p.sc, sx[r][e], f) : sx[r][e] * f;
+        if (MODS && p.sc.biased) {
+          const int j = key0 + g + 8 * (e >> 1);
+          sx[r][e] -= slope[2 * r + (e & 1)] * fabsf(static_cast<float>(pos[2 * r + (e & 1)] - j));
+        }
+      }
     const bool all_seen = mt.z != 0.f && (key0 + 16 <= kr.prefix ||
                                           (key0 + 15 <= p_lo && key0 + 16 <= s.len &&
                                            (p.sc.window == 0 || p_hi - key0 < p.sc.window)));
     if (!all_seen) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = key0 + 2 * t + (e & 1) + 8 * (e >> 1);
-          if (mt.z == 0.f || !row_sees(p.sc, kr, s.len, pos[r], j)) x[r][e] = -INFINITY;
+          const int j = key0 + g + 8 * (e >> 1);
+          if (mt.z == 0.f || !row_sees(p.sc, kr, s.len, pos[2 * r + (e & 1)], j)) sx[r][e] = -INFINITY;
         }
     }
     const float vs = E4M3 ? mt.y : 1.f, c2 = E4M3 ? scale_exponent(vs) : 0.f;
-    float mx[2];
+    bool raise = false;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) mx[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])) + c2;
-    if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
-      float al[2];
+    for (int q = 0; q < 2 * NR; ++q)
+      raise = raise || fmaxf(sx[q >> 1][q & 1], sx[q >> 1][2 + (q & 1)]) + c2 > m[q] + 8.f;
+    if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        const float nm = fmaxf(m[r], mx[r]);
-        al[r] = nm == -INFINITY ? 1.f : ex2(m[r] - nm);
-        m[r] = nm;
-        l[r] *= al[r];
-      }
+      for (int q = 0; q < 2 * NR; ++q) {
+        float mx = fmaxf(sx[q >> 1][q & 1], sx[q >> 1][2 + (q & 1)]) + c2;
 #pragma unroll
-      for (int n = 0; n < TR::NT; ++n) {
-        o[n][0] *= al[0];
-        o[n][1] *= al[0];
-        o[n][2] *= al[1];
-        o[n][3] *= al[1];
+        for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float nm = fmaxf(m[q], mx);
+        const float al = nm == -INFINITY ? 1.f : ex2(m[q] - nm);
+        m[q] = nm;
+        l[q] *= al;
+#pragma unroll
+        for (int n = 0; n < MT; ++n) {
+          o[q >> 1][n][q & 1] *= al;
+          o[q >> 1][n][2 + (q & 1)] *= al;
+        }
       }
     }
-    uint32_t pa[4];
+    uint32_t pb[NR][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float ms = m[r] == -INFINITY ? 0.f : m[r];
-      float e0 = ex2(x[r][0] - ms), e1 = ex2(x[r][1] - ms), e2 = ex2(x[r][2] - ms), e3 = ex2(x[r][3] - ms);
-      l[r] += (e0 + e1) + (e2 + e3);
+    for (int r = 0; r < NR; ++r) {
+      const float m0 = m[2 * r] == -INFINITY ? 0.f : m[2 * r], m1 = m[2 * r + 1] == -INFINITY ? 0.f : m[2 * r + 1];
+      const float e0 = ex2(sx[r][0] - m0), e1 = ex2(sx[r][1] - m1), e2 = ex2(sx[r][2] - m0), e3 = ex2(sx[r][3] - m1);
+      l[2 * r] += e0 + e2;
+      l[2 * r + 1] += e1 + e3;
       if constexpr (E4M3) {
-        pa[r] = pack_f16(e0 * vs, e1 * vs);
-        pa[2 + r] = pack_f16(e2 * vs, e3 * vs);
+        pb[r][0] = transpose8x8(pack_f16(e0 * vs, e1 * vs));
+        pb[r][1] = transpose8x8(pack_f16(e2 * vs, e3 * vs));
       } else {
-        pa[r] = pack_bf16(e0, e1);
-        pa[2 + r] = pack_bf16(e2, e3);
+        pb[r][0] = transpose8x8(pack_bf16(e0, e1));
+        pb[r][1] = transpose8x8(pack_bf16(e2, e3));
       }
     }
-    // O += P V
-    if constexpr (E4M3 && CH == 4) {  // D = 64: half a chunk per lane
-      uint32_t w[4][2];
+    // O^T += V^T P^T; words w[q] of key 2t, 2t+1, 2t+8, 2t+9
+    auto pv = [&](int n, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) mma16816<E4M3>(o[r][n], a0, a1, a2, a3, pb[r][0], pb[r][1]);
+    };
+    auto pv_word = [&](int n, const uint32_t (&w)[4]) {
+      if constexpr (E4M3) {  // four d: two MMAs
+        uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+        e4m3x4_f16(__byte_perm(w[0], w[1], 0x5140), x0, x1);
+        e4m3x4_f16(__byte_perm(w[0], w[1], 0x7362), x2, x3);
+        e4m3x4_f16(__byte_perm(w[2], w[3], 0x5140), y0, y1);
+        e4m3x4_f16(__byte_perm(w[2], w[3], 0x7362), y2, y3);
+        pv(2 * n, x0, x1, y0, y1);
+        pv(2 * n + 1, x2, x3, y2, y3);
+      } else {  // two d: one MMA
+        pv(n, __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x5410),
+           __byte_perm(w[2], w[3], 0x7632));
+      }
+    };
+    if constexpr (CH == 4) {  // 64-byte rows: half a chunk per lane
+      uint2 u[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int row = 2 * t + (q & 1) + 8 * (q >> 1);
-        const uint2 u = *reinterpret_cast<const uint2*>(sv + row * TR::ROWB + (swz<CH>(row, g >> 1) << 4) + (g & 1) * 8);
-        w[q][0] = u.x;
-        w[q][1] = u.y;
+        u[q] = *reinterpret_cast<const uint2*>(sv + row * TR::ROWB + (swz<CH>(row, g >> 1) << 4) + (g & 1) * 8);
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        pv_e4m3(&o[4 * i], pa, w[0][i], w[1][i], w[2][i], w[3][i]);
-      }
+      pv_word(0, {u[0].x, u[1].x, u[2].x, u[3].x});
+      pv_word(1, {u[0].y, u[1].y, u[2].y, u[3].y});
     } else {
 #pragma unroll
       for (int i = 0; i < CH / 8; ++i) {
-        uint32_t w[4][4];
+        uint4 u[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int row = 2 * t + (q & 1) + 8 * (q >> 1);
-          const uint4 u = *reinterpret_cast<const uint4*>(sv + row * TR::ROWB + (swz<CH>(row, g + 8 * i) << 4));
-          w[q][0] = u.x;
-          w[q][1] = u.y;
-          w[q][2] = u.z;
-          w[q][3] = u.w;
+          u[q] = *reinterpret_cast<const uint4*>(sv + row * TR::ROWB + (swz<CH>(row, g + 8 * i) << 4));
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (E4M3) {
-            pv_e4m3(&o[4 * e], pa, w[0][e], w[1][e], w[2][e], w[3][e]);
-          } else {
-            mma16816<false>(o[i * 8 + 2 * e], pa, __byte_perm(w[0][e], w[1][e], 0x5410),
-                            __byte_perm(w[2][e], w[3][e], 0x5410));
-            mma16816<false>(o[i * 8 + 2 * e + 1], pa, __byte_perm(w[0][e], w[1][e], 0x7632),
-                            __byte_perm(w[2][e], w[3][e], 0x7632));
-          }
-        }
+        pv_word(4 * i, {u[0].x, u[1].x, u[2].x, u[3].x});
+        pv_word(4 * i + 1, {u[0].y, u[1].y, u[2].y, u[3].y});
+        pv_word(4 * i + 2, {u[0].z, u[1].z, u[2].z, u[3].z});
+        pv_word(4 * i + 3, {u[0].w, u[1].w, u[2].w, u[3].w});
       }
     }
     __syncwarp();  // every lane is done with the stage
@@ -522,47 +531,46 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   // ---- join the block's warps
   cp_async_wait<0>();
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-  }
-  if (t == 0) {
-    s_m[warp * 16 + g] = m[0];
-    s_m[warp * 16 + g + 8] = m[1];
-    s_l[warp * 16 + g] = l[0];
-    s_l[warp * 16 + g + 8] = l[1];
-  }
-  __syncthreads();
-  float* s_o = reinterpret_cast<float*>(s_ring);  // [NW][16][D]
+  for (int q = 0; q < 2 * NR; ++q)
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+    for (int w = 4; w < 32; w <<= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], w);
+  if (g == 0)
+#pragma unroll
+    for (int q = 0; q < 2 * NR; ++q) {
+      s_m[warp * ROWS + 2 * t + (q & 1) + 8 * (q >> 1)] = m[q];
+      s_l[warp * ROWS + 2 * t + (q & 1) + 8 * (q >> 1)] = l[q];
+    }
+  __syncthreads();
+  float* s_o = reinterpret_cast<float*>(s_ring);  // [NW][ROWS][D]
+#pragma unroll
+  for (int q = 0; q < 2 * NR; ++q) {
+    const int row = 2 * t + (q & 1) + 8 * (q >> 1);
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + g + 8 * r]);
-    const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - M);
-    float* dst = s_o + (warp * 16 + g + 8 * r) * D;
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * ROWS + row]);
+    const float f = m[q] == -INFINITY ? 0.f : ex2(m[q] - M);
+    float* dst = s_o + (warp * ROWS + row) * D;
 #pragma unroll
-    for (int n = 0; n < TR::NT; ++n) {
-      // column c (0..7) of MMA n is this d
-      auto d_of = [&](int c) { return E4M3 ? c * (D / 8) + n : (c + 8 * (n / 8)) * 8 + n % 8; };
-      dst[d_of(2 * t)] = o[n][2 * r] * f;
-      dst[d_of(2 * t + 1)] = o[n][2 * r + 1] * f;
+    for (int n = 0; n < MT; ++n) {
+      // the two d of MMA n in lane g
+      const int d = E4M3 ? g * (D / 8) + 2 * n : (g + 8 * (n / 4)) * 8 + 2 * (n % 4);
+      *reinterpret_cast<float2*>(dst + d) = make_float2(o[q >> 1][n][q & 1] * f, o[q >> 1][n][2 + (q & 1)] * f);
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * (D / 4); i += TR::THREADS) {
+  for (int i = threadIdx.x; i < ROWS * (D / 4); i += TR::THREADS) {
     const int r = i / (D / 4), d4 = i % (D / 4);
     const int row = r0 + r;
     if (row >= rows) break;
     float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + r]);
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * ROWS + r]);
 #pragma unroll
-    for (int w = 0; w < NW; ++w) L += M == -INFINITY ? 0.f : s_l[w * 16 + r] * ex2(s_m[w * 16 + r] - M);
+    for (int w = 0; w < NW; ++w) L += M == -INFINITY ? 0.f : s_l[w * ROWS + r] * ex2(s_m[w * ROWS + r] - M);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float4 u = *reinterpret_cast<const float4*>(s_o + (w * 16 + r) * D + d4 * 4);
+      const float4 u = *reinterpret_cast<const float4*>(s_o + (w * ROWS + r) * D + d4 * 4);
       a.x += u.x;
       a.y += u.y;
       a.z += u.z;
