@@ -112,6 +112,16 @@ ll_status allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
 // bounds alone, so the workspace size is known before the call.
 constexpr int kDecodeRows = 32;  // rows of a sequence and K/V head up to which the decode kernel is taken
 
+// Blocks of the decode kernel that an SM holds.
+int decode_blocks(const ll_paged_cache* c, int rows) {
+  const bool e4m3 = c->dtype == LL_FP8_E4M3;
+  if (c->D == 128)
+    return e4m3 ? (rows == 8 ? ll::DecodeTraits<128, true, 8>::BLOCKS : ll::DecodeTraits<128, true, 16>::BLOCKS)
+                : (rows == 8 ? ll::DecodeTraits<128, false, 8>::BLOCKS : ll::DecodeTraits<128, false, 16>::BLOCKS);
+  return e4m3 ? (rows == 8 ? ll::DecodeTraits<64, true, 8>::BLOCKS : ll::DecodeTraits<64, true, 16>::BLOCKS)
+              : (rows == 8 ? ll::DecodeTraits<64, false, 8>::BLOCKS : ll::DecodeTraits<64, false, 16>::BLOCKS);
+}
+
 struct AttnPlan {
   bool tiles;  // 128-row tensor-memory tiles; else 16-row warp tiles
   int row_tile, key_tile, row_tiles, chunk, nsplit;
@@ -132,10 +142,12 @@ AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq
   const long long units = static_cast<long long>(t->B) * c->H * (a.row_tiles > 0 ? a.row_tiles : 1);
   long long chunk = nt;
   if (!a.tiles) {
-    // about two waves of blocks, so that ragged lengths even out; no piece below 256
-    // keys (64 per warp), where the join would cost more than it saves
-    const long long slots = 3ll * num_sms();
-    chunk = nt * units / (2 * slots);
+    // whole waves of blocks, so that equal lengths leave no block over, and several,
+    // so that ragged ones even out; no piece below 256 keys (64 per warp), where the
+    // join would cost more than it saves
+    const long long slots = decode_blocks(c, a.row_tile) * static_cast<long long>(num_sms());
+    const long long pieces = 3 * slots / units;
+    chunk = pieces > 1 ? (nt + pieces - 1) / pieces : nt;
     if (chunk < 16) chunk = 16;
   } else {
     // one block per SM: the number of pieces with the least waves x tiles, with 4
@@ -332,9 +344,12 @@ ll_status ll_paged_append(const ll_paged_cache* cache, const ll_token_batch* bat
   }
   const int units = ps * (cache->D / 16);  // 16-element units of a page and head
   p.head_threads = units < ll::kPagedAppendThreads ? units : ll::kPagedAppendThreads;
-  p.heads = ll::kPagedAppendThreads / p.head_threads;
+  const int side = ll::kPagedAppendThreads / p.head_threads;
   // pages that max_q tokens can touch, wherever the first of them stands
   const int touched = (max_q - 1) / ps + ((max_q - 1) % ps != 0 ? 2 : 1);
+  // as many heads per block as leave 4 blocks to an SM
+  const long long rounds = static_cast<long long>(touched) * batch->B * ((cache->H + side - 1) / side) / (4 * num_sms());
+  p.heads = side * static_cast<int>(rounds < 1 ? 1 : (rounds < cache->H ? rounds : cache->H));
   const dim3 grid(touched, batch->B, (cache->H + p.heads - 1) / p.heads);
   const size_t smem = static_cast<size_t>(max_q < ps ? max_q : ps) * pairs * sizeof(float2);
   auto launch = [&](auto kern, std::atomic<unsigned long long>& done) -> ll_status {

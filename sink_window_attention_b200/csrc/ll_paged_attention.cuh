@@ -205,10 +205,12 @@ struct DecodeTraits {
   static constexpr int TILE = 16 * ROWB;
   static constexpr int NW = 4;
   static constexpr int THREADS = NW * 32;
-  static constexpr int STAGES = ROWB >= 256 ? 3 : 4;
+  static constexpr int STAGES = ROWB >= 256 || ROWS == 8 ? 3 : 4;
   static constexpr int RING = NW * STAGES * 2 * TILE;
   static constexpr int QP = D + 8;          // 16-bit elements between rows of Q
-  static constexpr int BLOCKS = ROWB >= 256 ? 2 : 3;  // per SM, by shared memory
+  // Per SM, by shared memory and registers. 8 rows over 128-byte rows of K: 4 blocks
+  // with 3 stages each read 5.6 TB/s, 3 with 4 stages 4.4, 4 with 2 stages 5.4.
+  static constexpr int BLOCKS = ROWB >= 256 ? 2 : (ROWS == 8 ? 4 : 3);
   static constexpr int META = NW * STAGES * 16;
   static constexpr int SMEM = RING + META + ROWS * QP * 2 + ROWS * 4 + 2 * NW * ROWS * 4;
   static_assert(NW * ROWS * D * 4 <= RING, "the warps' O must fit the ring");
@@ -390,11 +392,12 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     const float4 mt = *reinterpret_cast<const float4*>(s_meta + (warp * STAGES + st) * 4);
     const int key0 = kr.tile(t_beg + k * NW) * 16;
     // S^T: [key g: row 2t, 2t+1][key g + 8: row 2t, 2t+1]
-    float sx[NR][4];
+    // (two accumulators, so that the MMAs' latencies overlap)
+    float sx[NR][4], sy[NR][4];
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sx[r][e] = 0.f;
+      for (int e = 0; e < 4; ++e) sx[r][e] = sy[r][e] = 0.f;
 #pragma unroll
     for (int i = 0; i < TR::KC; ++i) {
       const int ch = swz<CH>(g, t + 4 * i) << 4;  // g + 8 is swizzled like g
@@ -408,14 +411,15 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
           e4m3x4_f16(ua[e], a0, a2);
           e4m3x4_f16(wa[e], a1, a3);
 #pragma unroll
-          for (int r = 0; r < NR; ++r) mma16816<true>(sx[r], a0, a1, a2, a3, bq[r][i * 4 + e][0], bq[r][i * 4 + e][1]);
+          for (int r = 0; r < NR; ++r)
+            mma16816<true>(e & 1 ? sy[r] : sx[r], a0, a1, a2, a3, bq[r][i * 4 + e][0], bq[r][i * 4 + e][1]);
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int r = 0; r < NR; ++r)
-            mma16816<false>(sx[r], ua[2 * e], wa[2 * e], ua[2 * e + 1], wa[2 * e + 1], bq[r][i * 2 + e][0],
+            mma16816<false>(e & 1 ? sy[r] : sx[r], ua[2 * e], wa[2 * e], ua[2 * e + 1], wa[2 * e + 1], bq[r][i * 2 + e][0],
                             bq[r][i * 2 + e][1]);
       }
     }
@@ -425,8 +429,8 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float f = fac[2 * r + (e & 1)] * ks;
-        sx[r][e] = MODS ? score2(p.sc, sx[r][e], f) : sx[r][e] * f;
+        const float f = fac[2 * r + (e & 1)] * ks, y = sx[r][e] + sy[r][e];
+        sx[r][e] = MODS ? score2(p.sc, y, f) : y * f;
         if (MODS && p.sc.biased) {
           const int j = key0 + g + 8 * (e >> 1);
           sx[r][e] -= slope[2 * r + (e & 1)] * fabsf(static_cast<float>(pos[2 * r + (e & 1)] - j));

@@ -180,7 +180,7 @@ struct PagedAppendParams {
   TokenBatch batch;
   TokenRope rope;
   int tokens;          // bf16 pool: tokens per block
-  int heads, head_threads;  // 8-bit pool: heads per block, threads per head
+  int heads, head_threads;  // 8-bit pool: heads per block (a multiple of those side by side), threads per head
 };
 
 constexpr int kPagedAppendThreads = 256;
@@ -264,13 +264,25 @@ __device__ __forceinline__ uint2 recode8(uint2 c, float ratio) {
   return encode8(x, ratio);
 }
 
-// 8-bit pool: a block takes one page of one sequence and `heads` heads of it;
-// head_threads threads hold a head's new K and V in registers (IPT units of 16
-// elements each), so the maximum over the page and the codes come from one read.
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// 8-bit pool: a block takes one page of one sequence and `heads` heads of it, `side`
+// of them at a time: head_threads threads hold a head's new K and V in registers (IPT
+// units of 16 elements each), so the maximum over the page and the codes come from one
+// read, and the loads of the next heads are in flight meanwhile. The angles are
+// computed once for all heads (a block per head spent most of its time on them).
 template <int IPT>
 __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_e4m3_kernel(const PagedAppendParams p) {
-  extern __shared__ float2 s_cs[];                    // [new tokens of the page][rot / 2]
-  __shared__ float s_max[2][kPagedAppendThreads / 32];  // [K, V][warp]
+  extern __shared__ float2 s_cs[];                         // [new tokens of the page][rot / 2]
+  __shared__ float s_max[2][2][kPagedAppendThreads / 32];  // [parity][K, V][warp]
   const int b = blockIdx.y, ps = p.pool.page_size, D = p.pool.D, H = p.pool.H;
   const SeqView s = seq_view(p.batch, b, ps);
   // page number within the sequence, and the rows of it that are new
@@ -282,103 +294,115 @@ __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_e4m3_kernel(
   const int n1 = static_cast<int>((end < (pg + 1) * ps ? end : (pg + 1) * ps) - pg * ps);
   const int page = page_of(p.batch, b, static_cast<int>(pg), p.pool.n_pages);
   if (page < 0) return;
-  const int pairs = p.rope.rot >> 1;
+  const int per_head = D >> 4, pairs = p.rope.rot >> 1;
+  const int side = kPagedAppendThreads / p.head_threads;
+  const int slot_h = threadIdx.x / p.head_threads, lt = threadIdx.x - slot_h * p.head_threads;
+  const int h_end = min(H, static_cast<int>(blockIdx.z + 1) * p.heads);
+  const long long row0 = s.q0 + (pg * ps - s.first_pos);  // token-tensor row of the page's row 0
+  // this thread's units: row of the page, chunks lo and hi of the head
+  int slot[IPT], lo[IPT], hi[IPT];
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const int it = lt + i * p.head_threads;
+    slot[i] = it / per_head;
+    item_chunks(p.rope, it - slot[i] * per_head, lo[i], hi[i]);
+  }
+  uint4 raw[IPT][4];  // K lo, K hi, V lo, V hi
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {
+      if (h >= h_end || slot[i] < n0 || slot[i] >= n1) continue;
+      const __nv_bfloat16* kr = p.k + (row0 + slot[i]) * p.k_stride + h * D;
+      const __nv_bfloat16* vr = p.v + (row0 + slot[i]) * p.v_stride + h * D;
+      raw[i][0] = *reinterpret_cast<const uint4*>(kr + lo[i] * 8);
+      raw[i][1] = *reinterpret_cast<const uint4*>(kr + hi[i] * 8);
+      raw[i][2] = *reinterpret_cast<const uint4*>(vr + lo[i] * 8);
+      raw[i][3] = *reinterpret_cast<const uint4*>(vr + hi[i] * 8);
+    }
+  };
+  const int h0 = blockIdx.z * p.heads + slot_h;
+  load(h0);
   for (int i = threadIdx.x; i < (n1 - n0) * pairs; i += blockDim.x) {
     const int t = i / pairs;
     s_cs[i] = turn_of(p.rope, pg * ps + n0 + t, i - t * pairs);
   }
-  const int per_head = D >> 4;
-  const int slot_h = threadIdx.x / p.head_threads, lt = threadIdx.x - slot_h * p.head_threads;
-  const int h = blockIdx.z * p.heads + slot_h;
-  const bool live = slot_h < p.heads && h < H;
-  const long long row0 = s.q0 + (pg * ps - s.first_pos);  // token-tensor row of the page's row 0
-  const size_t head_at = (static_cast<size_t>(page) * H + (live ? h : 0)) * ps * D;
-  const size_t scale_at = static_cast<size_t>(page) * H + (live ? h : 0);
-  float was[2] = {0.f, 0.f};
-  if (live && n0 > 0) {
-    was[0] = p.pool.k_scale[scale_at];
-    was[1] = p.pool.v_scale[scale_at];
-  }
-  float x[IPT][4][8];  // K lo, K hi, V lo, V hi
-  float amax[2] = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < IPT; ++i) {
-    const int it = lt + i * p.head_threads;
-    const int slot = it / per_head, c = it - slot * per_head;
-    if (!live || slot < n0 || slot >= n1) continue;
-    int lo, hi;
-    item_chunks(p.rope, c, lo, hi);
-    const __nv_bfloat16* kr = p.k + (row0 + slot) * p.k_stride + h * D;
-    const __nv_bfloat16* vr = p.v + (row0 + slot) * p.v_stride + h * D;
-    load_chunk8<__nv_bfloat16>(kr + lo * 8, x[i][0]);
-    load_chunk8<__nv_bfloat16>(kr + hi * 8, x[i][1]);
-    load_chunk8<__nv_bfloat16>(vr + lo * 8, x[i][2]);
-    load_chunk8<__nv_bfloat16>(vr + hi * 8, x[i][3]);
-  }
-  __syncthreads();  // s_cs
-#pragma unroll
-  for (int i = 0; i < IPT; ++i) {
-    const int it = lt + i * p.head_threads;
-    const int slot = it / per_head, c = it - slot * per_head;
-    if (!live || slot < n0 || slot >= n1) continue;
-    if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x[i][0], x[i][1], s_cs + (slot - n0) * pairs + c * 8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      amax[0] = fmax3(amax[0], finite_abs(x[i][0][e]), finite_abs(x[i][1][e]));
-      amax[1] = fmax3(amax[1], finite_abs(x[i][2][e]), finite_abs(x[i][3][e]));
-    }
-  }
-  // head_threads is a multiple of 32: a warp holds one head
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    amax[0] = fmaxf(amax[0], __shfl_xor_sync(0xffffffffu, amax[0], o));
-    amax[1] = fmaxf(amax[1], __shfl_xor_sync(0xffffffffu, amax[1], o));
-  }
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
-    s_max[0][warp] = amax[0];
-    s_max[1][warp] = amax[1];
-  }
   __syncthreads();
-  if (!live) return;
-  float scale[2], inv[2], ratio[2];
+  int parity = 0;
+  for (int hb = blockIdx.z * p.heads; hb < h_end; hb += side, parity ^= 1) {
+    const int h = hb + slot_h;
+    const bool live = h < h_end;
+    const size_t scale_at = static_cast<size_t>(page) * H + (live ? h : 0);
+    float was[2] = {0.f, 0.f};
+    if (live && n0 > 0) {
+      was[0] = p.pool.k_scale[scale_at];
+      was[1] = p.pool.v_scale[scale_at];
+    }
+    float x[IPT][4][8];
+    float amax[2] = {0.f, 0.f};
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    float m = 0.f;
-    for (int i = slot_h * (p.head_threads >> 5); i < (slot_h + 1) * (p.head_threads >> 5); ++i) m = fmaxf(m, s_max[w][i]);
-    scale[w] = fmaxf(was[w], two_power_scale(m));
-    inv[w] = scale[w] > 0.f ? 1.0f / scale[w] : 0.f;
-    ratio[w] = was[w] * inv[w];
-  }
+    for (int i = 0; i < IPT; ++i) {
+      if (!live || slot[i] < n0 || slot[i] >= n1) continue;
 #pragma unroll
-  for (int i = 0; i < IPT; ++i) {
-    const int it = lt + i * p.head_threads;
-    const int slot = it / per_head, c = it - slot * per_head;
-    if (slot >= n1) continue;
-    if (slot >= n0) {
-      int lo, hi;
-      item_chunks(p.rope, c, lo, hi);
-      uint8_t* kd = static_cast<uint8_t*>(p.pool.k) + head_at + static_cast<size_t>(slot) * D;
-      uint8_t* vd = static_cast<uint8_t*>(p.pool.v) + head_at + static_cast<size_t>(slot) * D;
-      *reinterpret_cast<uint2*>(kd + lo * 8) = encode8(x[i][0], inv[0]);
-      *reinterpret_cast<uint2*>(kd + hi * 8) = encode8(x[i][1], inv[0]);
-      *reinterpret_cast<uint2*>(vd + lo * 8) = encode8(x[i][2], inv[1]);
-      *reinterpret_cast<uint2*>(vd + hi * 8) = encode8(x[i][3], inv[1]);
-    } else {
+      for (int w = 0; w < 4; ++w) unpack8(raw[i][w], x[i][w]);
+      const int c = (lt + i * p.head_threads) - slot[i] * per_head;
+      if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x[i][0], x[i][1], s_cs + (slot[i] - n0) * pairs + c * 8);
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (!(scale[w] > was[w])) continue;  // the earlier tokens' codes stand
-        uint2* cd = reinterpret_cast<uint2*>(static_cast<uint8_t*>(w ? p.pool.v : p.pool.k) + head_at +
-                                             static_cast<size_t>(slot) * D + c * 16);
-        const uint2 c0 = cd[0], c1 = cd[1];
-        cd[0] = recode8(c0, ratio[w]);
-        cd[1] = recode8(c1, ratio[w]);
+      for (int e = 0; e < 8; ++e) {
+        amax[0] = fmax3(amax[0], finite_abs(x[i][0][e]), finite_abs(x[i][1][e]));
+        amax[1] = fmax3(amax[1], finite_abs(x[i][2][e]), finite_abs(x[i][3][e]));
       }
     }
-  }
-  if (lt == 0) {
-    p.pool.k_scale[scale_at] = scale[0];
-    p.pool.v_scale[scale_at] = scale[1];
+    load(h + side);
+    // head_threads is a multiple of 32: a warp holds one head
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      amax[0] = fmaxf(amax[0], __shfl_xor_sync(0xffffffffu, amax[0], o));
+      amax[1] = fmaxf(amax[1], __shfl_xor_sync(0xffffffffu, amax[1], o));
+    }
+    if ((threadIdx.x & 31) == 0) {
+      s_max[parity][0][threadIdx.x >> 5] = amax[0];
+      s_max[parity][1][threadIdx.x >> 5] = amax[1];
+    }
+    __syncthreads();  // one per round: the next round writes the other parity
+    if (!live) continue;
+    float scale[2], inv[2], ratio[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float m = 0.f;
+      for (int i = slot_h * (p.head_threads >> 5); i < (slot_h + 1) * (p.head_threads >> 5); ++i)
+        m = fmaxf(m, s_max[parity][w][i]);
+      scale[w] = fmaxf(was[w], two_power_scale(m));
+      inv[w] = scale[w] > 0.f ? 1.0f / scale[w] : 0.f;
+      ratio[w] = was[w] * inv[w];
+    }
+    const size_t head_at = scale_at * ps * D;
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {
+      if (slot[i] >= n1) continue;
+      if (slot[i] >= n0) {
+        uint8_t* kd = static_cast<uint8_t*>(p.pool.k) + head_at + static_cast<size_t>(slot[i]) * D;
+        uint8_t* vd = static_cast<uint8_t*>(p.pool.v) + head_at + static_cast<size_t>(slot[i]) * D;
+        *reinterpret_cast<uint2*>(kd + lo[i] * 8) = encode8(x[i][0], inv[0]);
+        *reinterpret_cast<uint2*>(kd + hi[i] * 8) = encode8(x[i][1], inv[0]);
+        *reinterpret_cast<uint2*>(vd + lo[i] * 8) = encode8(x[i][2], inv[1]);
+        *reinterpret_cast<uint2*>(vd + hi[i] * 8) = encode8(x[i][3], inv[1]);
+      } else {
+        const int c = (lt + i * p.head_threads) - slot[i] * per_head;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (!(scale[w] > was[w])) continue;  // the earlier tokens' codes stand
+          uint2* cd = reinterpret_cast<uint2*>(static_cast<uint8_t*>(w ? p.pool.v : p.pool.k) + head_at +
+                                               static_cast<size_t>(slot[i]) * D + c * 16);
+          const uint2 c0 = cd[0], c1 = cd[1];
+          cd[0] = recode8(c0, ratio[w]);
+          cd[1] = recode8(c1, ratio[w]);
+        }
+      }
+    }
+    if (lt == 0) {
+      p.pool.k_scale[scale_at] = scale[0];
+      p.pool.v_scale[scale_at] = scale[1];
+    }
   }
 }
 
