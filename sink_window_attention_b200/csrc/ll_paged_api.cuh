@@ -301,7 +301,7 @@ ll_status ll_token_rope_apply(const void* x, long long x_stride, void* out, long
   tokens = tokens < fill ? tokens : fill;
   p.tokens = tokens < 1 ? 1 : (tokens > 8 ? 8 : tokens);
   const int grid = (T - 1) / p.tokens + 1;
-  const size_t smem = static_cast<size_t>(p.tokens) * (p.rope.rot / 2) * sizeof(float2);
+  const size_t smem = ll::turn_table_bytes(p.tokens, p.rope.rot / 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == LL_F32)
     ll::token_rope_kernel<float><<<grid, ll::kTokenRopeThreads, smem, s>>>(p);
@@ -339,31 +339,23 @@ ll_status ll_paged_append(const ll_paged_cache* cache, const ll_token_batch* bat
     if (tokens > fill) tokens = static_cast<int>(fill);
     p.tokens = tokens < 1 ? 1 : (tokens > 16 ? 16 : tokens);
     ll::paged_append_bf16_kernel<<<dim3((max_q - 1) / p.tokens + 1, batch->B), ll::kPagedAppendThreads,
-                                   static_cast<size_t>(p.tokens) * pairs * sizeof(float2), s>>>(p);
+                                   ll::turn_table_bytes(p.tokens, pairs), s>>>(p);
     return check_launch("paged_append_bf16_kernel");
   }
-  const int units = ps * (cache->D / 16);  // 16-element units of a page and head
-  p.head_threads = units < ll::kPagedAppendThreads ? units : ll::kPagedAppendThreads;
-  const int side = ll::kPagedAppendThreads / p.head_threads;
+  const int units = ps * (cache->D / 16);  // 16-element units of a page and head: 64 to 1024
+  const int side = units < 128 ? 128 / units : 1;
   // pages that max_q tokens can touch, wherever the first of them stands
   const int touched = (max_q - 1) / ps + ((max_q - 1) % ps != 0 ? 2 : 1);
-  // as many heads per block as leave 4 blocks to an SM
-  const long long rounds = static_cast<long long>(touched) * batch->B * ((cache->H + side - 1) / side) / (4 * num_sms());
-  p.heads = side * static_cast<int>(rounds < 1 ? 1 : (rounds < cache->H ? rounds : cache->H));
-  const dim3 grid(touched, batch->B, (cache->H + p.heads - 1) / p.heads);
-  const size_t smem = static_cast<size_t>(max_q < ps ? max_q : ps) * pairs * sizeof(float2);
-  auto launch = [&](auto kern, std::atomic<unsigned long long>& done) -> ll_status {
-    const ll_status a = allow_smem(kern, 128 * LL_MAX_TOKEN_PAIRS * static_cast<int>(sizeof(float2)), done);
-    if (a != LL_OK) return a;
-    kern<<<grid, ll::kPagedAppendThreads, smem, s>>>(p);
-    return check_launch("paged_append_e4m3_kernel");
-  };
-  static std::atomic<unsigned long long> done[3];
-  switch (units / p.head_threads) {
-    case 1: return launch(ll::paged_append_e4m3_kernel<1>, done[0]);
-    case 2: return launch(ll::paged_append_e4m3_kernel<2>, done[1]);
-    default: return launch(ll::paged_append_e4m3_kernel<4>, done[2]);
-  }
+  // heads per block: doubled while that divides them and leaves 4 blocks to an SM
+  const long long pages = static_cast<long long>(touched) * batch->B;
+  p.heads = side;
+  while (cache->H % (2 * p.heads) == 0 && pages * (cache->H / (2 * p.heads)) >= 4 * num_sms()) p.heads *= 2;
+  static std::atomic<unsigned long long> done{0};
+  st = allow_smem(ll::paged_append_e4m3_kernel, static_cast<int>(ll::turn_table_bytes(128, LL_MAX_TOKEN_PAIRS)), done);
+  if (st != LL_OK) return st;
+  ll::paged_append_e4m3_kernel<<<dim3(touched, batch->B, (cache->H + p.heads - 1) / p.heads), side * units,
+                                 ll::turn_table_bytes(max_q < ps ? max_q : ps, pairs), s>>>(p);
+  return check_launch("paged_append_e4m3_kernel");
 }
 
 size_t ll_paged_attention_workspace_bytes(const ll_paged_cache* cache, const ll_token_batch* batch, int Hq) {

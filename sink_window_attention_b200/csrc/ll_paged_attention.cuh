@@ -295,6 +295,11 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   for (int k = 0; k < STAGES - 1; ++k) issue(k);
 
   // ---- Q: rotated in fp32, rounded to the MMA's type
+  __shared__ unsigned long long s_turns[kMaxTokenPairs];
+  if (p.rope.rot > 0) {
+    if (threadIdx.x < p.rope.rot >> 1) s_turns[threadIdx.x] = p.rope.turns[threadIdx.x];
+    __syncthreads();
+  }
   for (int i = threadIdx.x; i < ROWS * (D / 16); i += TR::THREADS) {
     const int r = i / (D / 16), c = i % (D / 16);
     const int row = r0 + r, tok = row / p.group, h = hkv * p.group + row % p.group;
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
       if (c < (p.rope.rot >> 4)) {
         float2 cs[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) cs[e] = turn_of(p.rope, s.first_pos + tok, c * 8 + e);
-        rotate_item(p.rope, x, y, cs);
+        for (int e = 0; e < 8; ++e) cs[e] = turn_of(p.rope, s.first_pos + tok, s_turns[c * 8 + e]);
+        rotate_item(p.rope, x, y, cs, 1);
       }
     }
     uint32_t w[8];

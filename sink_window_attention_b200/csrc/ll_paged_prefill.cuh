@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
               float2 cs[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) cs[e] = turn_fast(p.rope, pos, c * 8 + e);
-              rotate_item(p.rope, x, y, cs);
+              rotate_item(p.rope, x, y, cs, 1);
             }
           }
           uint32_t u[8];

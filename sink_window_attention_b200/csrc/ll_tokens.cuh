@@ -62,13 +62,13 @@ struct TokenRope {
   unsigned long long turns[kMaxTokenPairs];
 };
 
-// (cos, sin) of pair i at position `pos`, times the amplitude. The turn is
-// pos * turns[i] modulo 2^64: exact, so a far position costs no accuracy (a
+// (cos, sin) of a pair at position `pos`, times the amplitude. The angle in turns is
+// pos * turn modulo 2^64: exact, so a far position costs no accuracy (a
 // product of an fp32 position and frequency would be off by 0.03 rad at
 // position 10^6). The nearest quarter turn is taken off in integers, so the rest
 // (at most an eighth of a turn) keeps all of fp32's bits.
-__device__ __forceinline__ float2 turn_of(const TokenRope& r, long long pos, int i) {
-  const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * r.turns[i]) >> 32);
+__device__ __forceinline__ float2 turn_of(const TokenRope& r, long long pos, unsigned long long turn) {
+  const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * turn) >> 32);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
   const float a = static_cast<float>(static_cast<int>(t - (quarter << 30))) * 4.656612873077393e-10f;  // half turns
   float s, c;
@@ -93,11 +93,12 @@ __device__ __forceinline__ void item_chunks(const TokenRope& r, int c, int& lo, 
   }
 }
 
-__device__ __forceinline__ void rotate_item(const TokenRope& r, float (&a)[8], float (&b)[8], const float2* cs) {
+// cs: (cos, sin) of the unit's 8 pairs, `step` apart.
+__device__ __forceinline__ void rotate_item(const TokenRope& r, float (&a)[8], float (&b)[8], const float2* cs, int step) {
   if (r.half) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 t = cs[i];
+      const float2 t = cs[i * step];
       const float x = a[i], y = b[i];
       a[i] = x * t.x - y * t.y;
       b[i] = x * t.y + y * t.x;
@@ -105,7 +106,7 @@ __device__ __forceinline__ void rotate_item(const TokenRope& r, float (&a)[8], f
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 t = cs[i], u = cs[4 + i];
+      const float2 t = cs[i * step], u = cs[(4 + i) * step];
       float x = a[2 * i], y = a[2 * i + 1];
       a[2 * i] = x * t.x - y * t.y;
       a[2 * i + 1] = x * t.y + y * t.x;
@@ -115,6 +116,38 @@ __device__ __forceinline__ void rotate_item(const TokenRope& r, float (&a)[8], f
       b[2 * i + 1] = x * u.y + y * u.x;
     }
   }
+}
+
+// A block's table of (cos, sin): a row per token, pair 8c + e at [e][c], so that the
+// lanes of neighbouring units read neighbouring entries, and 8 entries between rows
+// for the units of the next tokens (64-byte reads straight from pair order met in the
+// same banks four at a time).
+struct TurnTable {
+  float2* cs;
+  int pairs, step;
+  __device__ __forceinline__ const float2* unit(int token, int c) const { return cs + token * (pairs + 8) + c; }
+};
+__host__ __device__ inline size_t turn_table_bytes(int tokens, int pairs) {
+  return pairs == 0 ? 0 : (static_cast<size_t>(tokens) * (pairs + 8) * sizeof(float2));
+}
+
+// Fills the table for `nt` tokens, position_of(t) giving their positions; two block
+// barriers. The turns come from shared memory: as an index into the kernel's
+// parameters that differs by lane each read would be served a lane at a time (that
+// took three quarters of the append's time).
+template <class F>
+__device__ __forceinline__ TurnTable make_turn_table(const TokenRope& r, float2* cs, int nt, F&& position_of) {
+  __shared__ unsigned long long s_turns[kMaxTokenPairs];
+  TurnTable tab{cs, r.rot >> 1, r.rot >> 4};
+  for (int i = threadIdx.x; i < tab.pairs; i += blockDim.x) s_turns[i] = r.turns[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * tab.pairs; i += blockDim.x) {
+    const int t = i / tab.pairs, j = i - t * tab.pairs;  // entry j of the row: pair 8 (j % step) + j / step
+    const int e = j / tab.step, c = j - e * tab.step;
+    cs[t * (tab.pairs + 8) + j] = turn_of(r, position_of(t), s_turns[c * 8 + e]);
+  }
+  __syncthreads();
+  return tab;
 }
 
 // ---------------------------------------------------------------------------
@@ -134,15 +167,10 @@ constexpr int kTokenRopeThreads = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(kTokenRopeThreads) token_rope_kernel(const TokenRopeParams p) {
-  extern __shared__ float2 s_cs[];  // [tokens][rot / 2]
-  const int pairs = p.rope.rot >> 1;
+  extern __shared__ float2 s_cs[];
   const int t0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, p.T - t0);
-  for (int i = threadIdx.x; i < nt * pairs; i += blockDim.x) {
-    const int t = i / pairs;
-    s_cs[i] = turn_of(p.rope, p.positions[t0 + t], i - t * pairs);
-  }
-  __syncthreads();
+  const TurnTable tab = make_turn_table(p.rope, s_cs, nt, [&](int t) { return static_cast<long long>(p.positions[t0 + t]); });
   const int per_head = p.D >> 4, per_token = p.H * per_head;
   const int items = nt * per_token;
   for (int i = threadIdx.x; i < items; i += blockDim.x) {
@@ -155,7 +183,7 @@ __global__ void __launch_bounds__(kTokenRopeThreads) token_rope_kernel(const Tok
     float a[8], b[8];
     load_chunk8<T>(src + lo * 8, a);
     load_chunk8<T>(src + hi * 8, b);
-    if (c < (p.rope.rot >> 4)) rotate_item(p.rope, a, b, s_cs + t * pairs + c * 8);
+    if (c < (p.rope.rot >> 4)) rotate_item(p.rope, a, b, tab.unit(t, c), tab.step);
     store_chunk8<T>(dst + lo * 8, a);
     store_chunk8<T>(dst + hi * 8, b);
   }
@@ -180,25 +208,21 @@ struct PagedAppendParams {
   TokenBatch batch;
   TokenRope rope;
   int tokens;          // bf16 pool: tokens per block
-  int heads, head_threads;  // 8-bit pool: heads per block (a multiple of those side by side), threads per head
+  int heads;   // 8-bit pool: heads per block, a multiple of those side by side
 };
 
 constexpr int kPagedAppendThreads = 256;
+constexpr int kPagedAppendMaxThreads = 1024;  // 8-bit pool: a thread per 16 elements of a page and head
 
 // BF16 pool: a block takes `tokens` tokens of one sequence, all heads.
 __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_bf16_kernel(const PagedAppendParams p) {
-  extern __shared__ float2 s_cs[];  // [tokens][rot / 2]
+  extern __shared__ float2 s_cs[];
   const int b = blockIdx.y;
   const SeqView s = seq_view(p.batch, b, p.pool.page_size);
   const int i0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, s.nq - i0);
   if (nt <= 0) return;
-  const int pairs = p.rope.rot >> 1;
-  for (int i = threadIdx.x; i < nt * pairs; i += blockDim.x) {
-    const int t = i / pairs;
-    s_cs[i] = turn_of(p.rope, s.first_pos + i0 + t, i - t * pairs);
-  }
-  __syncthreads();
+  const TurnTable tab = make_turn_table(p.rope, s_cs, nt, [&](int t) { return s.first_pos + i0 + t; });
   const int D = p.pool.D, H = p.pool.H, ps = p.pool.page_size;
   const int per_head = D >> 4, per_token = H * per_head;
   for (int i = threadIdx.x; i < nt * per_token; i += blockDim.x) {
@@ -217,7 +241,7 @@ __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_bf16_kernel(
     float x[8], y[8];
     load_chunk8<__nv_bfloat16>(kr + lo * 8, x);
     load_chunk8<__nv_bfloat16>(kr + hi * 8, y);
-    if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x, y, s_cs + t * pairs + c * 8);
+    if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x, y, tab.unit(t, c), tab.step);
     const size_t at = ((static_cast<size_t>(page) * H + h) * ps + static_cast<int>(pos % ps)) * D;
     __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(p.pool.k) + at;
     __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.pool.v) + at;
@@ -274,15 +298,28 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
   }
 }
 
+// The largest finite |x| of eight bf16 values: as integers, where an exponent of all
+// ones (infinity, NaN) counts as 0.
+__device__ __forceinline__ uint32_t bf16_amax(const uint4& u, uint32_t a) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] << 16 & 0x7FFF0000u, hi = w[i] & 0x7FFF0000u;
+    a = max(a, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+  }
+  return a;
+}
+
 // 8-bit pool: a block takes one page of one sequence and `heads` heads of it, `side`
-// of them at a time: head_threads threads hold a head's new K and V in registers (IPT
-// units of 16 elements each), so the maximum over the page and the codes come from one
-// read, and the loads of the next heads are in flight meanwhile. The angles are
-// computed once for all heads (a block per head spent most of its time on them).
-template <int IPT>
-__global__ void __launch_bounds__(kPagedAppendThreads) paged_append_e4m3_kernel(const PagedAppendParams p) {
-  extern __shared__ float2 s_cs[];                         // [new tokens of the page][rot / 2]
-  __shared__ float s_max[2][2][kPagedAppendThreads / 32];  // [parity][K, V][warp]
+// of them at a time, a thread per unit of 16 elements of a head's K and V. They stay in
+// registers between the maximum over the page and the codes, so each is read once;
+// the next heads' loads are issued before this round's barrier. The angles are computed
+// once for all heads of a block. Measured (8800 tokens, 8 heads of 128, pages of 64): a
+// block per head, 65 us; angles shared but two units per thread, so that registers left
+// one block per SM, 42 us.
+__global__ void __launch_bounds__(kPagedAppendMaxThreads, 1) paged_append_e4m3_kernel(const PagedAppendParams p) {
+  extern __shared__ float2 s_cs[];
+  __shared__ uint32_t s_max[2][2][kPagedAppendMaxThreads / 32];  // [parity][K, V][warp]: bits of the maximum
   const int b = blockIdx.y, ps = p.pool.page_size, D = p.pool.D, H = p.pool.H;
   const SeqView s = seq_view(p.batch, b, ps);
   // page number within the sequence, and the rows of it that are new
@@ -294,39 +331,28 @@ __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_e4m3_kernel(
   const int n1 = static_cast<int>((end < (pg + 1) * ps ? end : (pg + 1) * ps) - pg * ps);
   const int page = page_of(p.batch, b, static_cast<int>(pg), p.pool.n_pages);
   if (page < 0) return;
-  const int per_head = D >> 4, pairs = p.rope.rot >> 1;
-  const int side = kPagedAppendThreads / p.head_threads;
-  const int slot_h = threadIdx.x / p.head_threads, lt = threadIdx.x - slot_h * p.head_threads;
+  const int per_head = D >> 4;
+  const int units = ps * per_head;  // of a head: a multiple of 32, so a warp holds one head
+  const int side = blockDim.x / units;
+  const int slot_h = threadIdx.x / units, lt = threadIdx.x - slot_h * units;
+  const int slot = lt / per_head, c = lt - slot * per_head;
+  int lo, hi;
+  item_chunks(p.rope, c, lo, hi);
+  const bool fresh = slot >= n0 && slot < n1;
   const int h_end = min(H, static_cast<int>(blockIdx.z + 1) * p.heads);
-  const long long row0 = s.q0 + (pg * ps - s.first_pos);  // token-tensor row of the page's row 0
-  // this thread's units: row of the page, chunks lo and hi of the head
-  int slot[IPT], lo[IPT], hi[IPT];
-#pragma unroll
-  for (int i = 0; i < IPT; ++i) {
-    const int it = lt + i * p.head_threads;
-    slot[i] = it / per_head;
-    item_chunks(p.rope, it - slot[i] * per_head, lo[i], hi[i]);
-  }
-  uint4 raw[IPT][4];  // K lo, K hi, V lo, V hi
+  const long long row = s.q0 + (pg * ps - s.first_pos) + slot;  // of the token tensors
+  const __nv_bfloat16* kr = p.k + row * p.k_stride;
+  const __nv_bfloat16* vr = p.v + row * p.v_stride;
+  uint4 raw[4];  // K lo, K hi, V lo, V hi
   auto load = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-      if (h >= h_end || slot[i] < n0 || slot[i] >= n1) continue;
-      const __nv_bfloat16* kr = p.k + (row0 + slot[i]) * p.k_stride + h * D;
-      const __nv_bfloat16* vr = p.v + (row0 + slot[i]) * p.v_stride + h * D;
-      raw[i][0] = *reinterpret_cast<const uint4*>(kr + lo[i] * 8);
-      raw[i][1] = *reinterpret_cast<const uint4*>(kr + hi[i] * 8);
-      raw[i][2] = *reinterpret_cast<const uint4*>(vr + lo[i] * 8);
-      raw[i][3] = *reinterpret_cast<const uint4*>(vr + hi[i] * 8);
-    }
+    if (!fresh || h >= h_end) return;
+    raw[0] = *reinterpret_cast<const uint4*>(kr + h * D + lo * 8);
+    raw[1] = *reinterpret_cast<const uint4*>(kr + h * D + hi * 8);
+    raw[2] = *reinterpret_cast<const uint4*>(vr + h * D + lo * 8);
+    raw[3] = *reinterpret_cast<const uint4*>(vr + h * D + hi * 8);
   };
-  const int h0 = blockIdx.z * p.heads + slot_h;
-  load(h0);
-  for (int i = threadIdx.x; i < (n1 - n0) * pairs; i += blockDim.x) {
-    const int t = i / pairs;
-    s_cs[i] = turn_of(p.rope, pg * ps + n0 + t, i - t * pairs);
-  }
-  __syncthreads();
+  load(blockIdx.z * p.heads + slot_h);
+  const TurnTable tab = make_turn_table(p.rope, s_cs, n1 - n0, [&](int t) { return pg * ps + n0 + t; });
   int parity = 0;
   for (int hb = blockIdx.z * p.heads; hb < h_end; hb += side, parity ^= 1) {
     const int h = hb + slot_h;
@@ -337,66 +363,52 @@ __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_e4m3_kernel(
       was[0] = p.pool.k_scale[scale_at];
       was[1] = p.pool.v_scale[scale_at];
     }
-    float x[IPT][4][8];
-    float amax[2] = {0.f, 0.f};
+    float x[8], y[8];  // K
+    const uint4 v0 = raw[2], v1 = raw[3];
+    uint32_t amax[2] = {0u, 0u};
+    if (live && fresh) {
+      unpack8(raw[0], x);
+      unpack8(raw[1], y);
+      if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x, y, tab.unit(slot - n0, c), tab.step);
+      float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-      if (!live || slot[i] < n0 || slot[i] >= n1) continue;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) unpack8(raw[i][w], x[i][w]);
-      const int c = (lt + i * p.head_threads) - slot[i] * per_head;
-      if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x[i][0], x[i][1], s_cs + (slot[i] - n0) * pairs + c * 8);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        amax[0] = fmax3(amax[0], finite_abs(x[i][0][e]), finite_abs(x[i][1][e]));
-        amax[1] = fmax3(amax[1], finite_abs(x[i][2][e]), finite_abs(x[i][3][e]));
-      }
+      for (int e = 0; e < 8; ++e) a = fmax3(a, finite_abs(x[e]), finite_abs(y[e]));
+      amax[0] = __float_as_uint(a);
+      amax[1] = bf16_amax(v1, bf16_amax(v0, 0u));
     }
     load(h + side);
-    // head_threads is a multiple of 32: a warp holds one head
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      amax[0] = fmaxf(amax[0], __shfl_xor_sync(0xffffffffu, amax[0], o));
-      amax[1] = fmaxf(amax[1], __shfl_xor_sync(0xffffffffu, amax[1], o));
-    }
-    if ((threadIdx.x & 31) == 0) {
-      s_max[parity][0][threadIdx.x >> 5] = amax[0];
-      s_max[parity][1][threadIdx.x >> 5] = amax[1];
+    for (int w = 0; w < 2; ++w) {  // non-negative floats order as integers
+      amax[w] = __reduce_max_sync(0xffffffffu, amax[w]);
+      if ((threadIdx.x & 31) == 0) s_max[parity][w][threadIdx.x >> 5] = amax[w];
     }
     __syncthreads();  // one per round: the next round writes the other parity
     if (!live) continue;
-    float scale[2], inv[2], ratio[2];
+    float scale[2], inv[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      float m = 0.f;
-      for (int i = slot_h * (p.head_threads >> 5); i < (slot_h + 1) * (p.head_threads >> 5); ++i)
-        m = fmaxf(m, s_max[parity][w][i]);
-      scale[w] = fmaxf(was[w], two_power_scale(m));
+      uint32_t m = 0u;
+      for (int i = slot_h * (units >> 5); i < (slot_h + 1) * (units >> 5); ++i) m = max(m, s_max[parity][w][i]);
+      scale[w] = fmaxf(was[w], two_power_scale(__uint_as_float(m)));
       inv[w] = scale[w] > 0.f ? 1.0f / scale[w] : 0.f;
-      ratio[w] = was[w] * inv[w];
     }
-    const size_t head_at = scale_at * ps * D;
+    uint8_t* kd = static_cast<uint8_t*>(p.pool.k) + scale_at * ps * D + static_cast<size_t>(slot) * D;
+    uint8_t* vd = static_cast<uint8_t*>(p.pool.v) + scale_at * ps * D + static_cast<size_t>(slot) * D;
+    if (fresh) {
+      *reinterpret_cast<uint2*>(kd + lo * 8) = encode8(x, inv[0]);
+      *reinterpret_cast<uint2*>(kd + hi * 8) = encode8(y, inv[0]);
+      unpack8(v0, x);
+      *reinterpret_cast<uint2*>(vd + lo * 8) = encode8(x, inv[1]);
+      unpack8(v1, x);
+      *reinterpret_cast<uint2*>(vd + hi * 8) = encode8(x, inv[1]);
+    } else if (slot < n0) {
 #pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-      if (slot[i] >= n1) continue;
-      if (slot[i] >= n0) {
-        uint8_t* kd = static_cast<uint8_t*>(p.pool.k) + head_at + static_cast<size_t>(slot[i]) * D;
-        uint8_t* vd = static_cast<uint8_t*>(p.pool.v) + head_at + static_cast<size_t>(slot[i]) * D;
-        *reinterpret_cast<uint2*>(kd + lo[i] * 8) = encode8(x[i][0], inv[0]);
-        *reinterpret_cast<uint2*>(kd + hi[i] * 8) = encode8(x[i][1], inv[0]);
-        *reinterpret_cast<uint2*>(vd + lo[i] * 8) = encode8(x[i][2], inv[1]);
-        *reinterpret_cast<uint2*>(vd + hi[i] * 8) = encode8(x[i][3], inv[1]);
-      } else {
-        const int c = (lt + i * p.head_threads) - slot[i] * per_head;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (!(scale[w] > was[w])) continue;  // the earlier tokens' codes stand
-          uint2* cd = reinterpret_cast<uint2*>(static_cast<uint8_t*>(w ? p.pool.v : p.pool.k) + head_at +
-                                               static_cast<size_t>(slot[i]) * D + c * 16);
-          const uint2 c0 = cd[0], c1 = cd[1];
-          cd[0] = recode8(c0, ratio[w]);
-          cd[1] = recode8(c1, ratio[w]);
-        }
+      for (int w = 0; w < 2; ++w) {
+        if (!(scale[w] > was[w])) continue;  // the earlier tokens' codes stand
+        uint2* cd = reinterpret_cast<uint2*>((w ? vd : kd) + c * 16);
+        const uint2 c0 = cd[0], c1 = cd[1];
+        cd[0] = recode8(c0, was[w] * inv[w]);
+        cd[1] = recode8(c1, was[w] * inv[w]);
       }
     }
     if (lt == 0) {
