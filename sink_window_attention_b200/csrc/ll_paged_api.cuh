@@ -72,7 +72,14 @@ ll_status check_rows(const char* what, const void* x, long long stride, int H, i
   return LL_OK;
 }
 
-ll::TokenBatch to_batch(const ll_token_batch* t) {
+// Keys of a sequence that may exist: the kernels round up to whole tiles in 32 bits.
+int max_key(const ll_token_batch* t, int page_size) {
+  const long long cap = static_cast<long long>(t->max_pages) * page_size;
+  const long long n = t->max_kv < cap ? t->max_kv : cap;
+  return static_cast<int>(n < INT_MAX - 256 ? n : INT_MAX - 256);
+}
+
+ll::TokenBatch to_batch(const ll_token_batch* t, int page_size) {
   ll::TokenBatch b;
   b.q_start = t->q_start;
   b.kv_len = t->kv_len;
@@ -81,7 +88,7 @@ ll::TokenBatch to_batch(const ll_token_batch* t) {
   b.max_pages = t->max_pages;
   b.total_q = t->total_q;
   b.max_q = t->max_q < t->total_q ? t->max_q : t->total_q;
-  b.max_kv = t->max_kv;
+  b.max_key = max_key(t, page_size);
   return b;
 }
 
@@ -93,6 +100,7 @@ ll::PagedPool to_pool(const ll_paged_cache* c) {
   p.v_scale = c->v_scale;
   p.n_pages = c->n_pages;
   p.page_size = c->page_size;
+  p.page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
   p.H = c->H;
   p.D = c->D;
   return p;
@@ -131,14 +139,13 @@ AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq
   AttnPlan a;
   const int group = Hq / c->H;
   const long long max_q = t->max_q < t->total_q ? t->max_q : t->total_q;
-  const long long cap = static_cast<long long>(t->max_pages) * c->page_size;
-  const long long max_kv = t->max_kv < cap ? t->max_kv : cap;
   a.tiles = max_q * group > kDecodeRows;
   a.row_tile = a.tiles ? 256 : (max_q * group <= 8 ? 8 : 16);
   a.key_tile = a.tiles ? 128 : 16;
   a.row_tiles = static_cast<int>((max_q * group + a.row_tile - 1) / a.row_tile);
   // at most (window and prefix only shorten a range)
-  const long long nt = max_kv > 0 ? (max_kv + a.key_tile - 1) / a.key_tile : 1;
+  const long long keys = max_key(t, c->page_size);
+  const long long nt = keys > 0 ? (keys + a.key_tile - 1) / a.key_tile : 1;
   const long long units = static_cast<long long>(t->B) * c->H * (a.row_tiles > 0 ? a.row_tiles : 1);
   long long chunk = nt;
   if (!a.tiles) {
@@ -327,7 +334,7 @@ ll_status ll_paged_append(const ll_paged_cache* cache, const ll_token_batch* bat
   p.k_stride = k_stride;
   p.v_stride = v_stride;
   p.pool = to_pool(cache);
-  p.batch = to_batch(batch);
+  p.batch = to_batch(batch, cache->page_size);
   const int max_q = p.batch.max_q;
   if (max_q == 0) return LL_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -414,7 +421,7 @@ ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype
   p.Hq = Hq;
   p.group = Hq / cache->H;
   p.pool = to_pool(cache);
-  p.batch = to_batch(batch);
+  p.batch = to_batch(batch, cache->page_size);
   p.row_tile = plan.row_tile;
   p.key_tile = plan.key_tile;
   p.row_tiles = plan.row_tiles;

@@ -53,15 +53,18 @@ struct KeyRange {
   __device__ __forceinline__ bool some_row_sees(int j) const { return j < always || (j >= lo && j < upper); }
 };
 
-__device__ __forceinline__ KeyRange key_range(const ScoreParams& sc, int b, const SeqView& s, long long p_lo,
-                                              long long p_hi, int key_tile) {
+// The first key that the window of position p reaches.
+__device__ __forceinline__ int window_begin(const ScoreParams& sc, int p) {
+  return sc.window > 0 && p >= sc.window ? p - sc.window + 1 : 0;
+}
+
+__device__ __forceinline__ KeyRange key_range(const ScoreParams& sc, int b, const SeqView& s, int p_lo, int p_hi,
+                                              int key_tile) {
   KeyRange r;
   int prefix = sc.prefix_len ? sc.prefix_len[b] : 0;
   r.prefix = prefix < 0 ? 0 : (prefix < s.len ? prefix : s.len);
-  const long long causal = p_hi + 1 < s.len ? p_hi + 1 : s.len;  // keys [0, causal) stand at or before the last row
-  r.upper = static_cast<int>(causal > 0 ? causal : 0);
-  const long long lo = sc.window > 0 ? p_lo - sc.window + 1 : 0;
-  r.lo = static_cast<int>(lo < 0 ? 0 : (lo < r.upper ? lo : r.upper));
+  r.upper = max(min(p_hi + 1, s.len), 0);  // keys [0, upper) stand at or before the last row
+  r.lo = min(window_begin(sc, p_lo), r.upper);
   const int sink = sc.window > 0 ? (sc.n_sink < r.upper ? sc.n_sink : r.upper) : 0;
   r.always = sink > r.prefix ? sink : r.prefix;
   r.a_end = (r.always + key_tile - 1) / key_tile;
@@ -72,14 +75,13 @@ __device__ __forceinline__ KeyRange key_range(const ScoreParams& sc, int b, cons
   return r;
 }
 
-__device__ __forceinline__ bool row_sees(const ScoreParams& sc, const KeyRange& r, int len, long long p, int j) {
+__device__ __forceinline__ bool row_sees(const ScoreParams& sc, const KeyRange& r, int len, int p, int j) {
   if (j < r.prefix) return true;
   return j <= p && j < len && (sc.window == 0 || p - j < sc.window || j < sc.n_sink);
 }
 
 // Positions of a unit's first and last row.
-__device__ __forceinline__ void unit_positions(const PagedAttnParams& p, const SeqView& s, int r0, long long& lo,
-                                               long long& hi) {
+__device__ __forceinline__ void unit_positions(const PagedAttnParams& p, const SeqView& s, int r0, int& lo, int& hi) {
   const int last = min(r0 + p.row_tile, s.nq * p.group) - 1;
   lo = s.first_pos + r0 / p.group;
   hi = s.first_pos + last / p.group;
@@ -88,6 +90,11 @@ __device__ __forceinline__ void unit_positions(const PagedAttnParams& p, const S
 __device__ __forceinline__ int piece_count(const PagedAttnParams& p, int nt) {
   const int n = (nt + p.chunk - 1) / p.chunk;
   return n > 1 ? n : 1;
+}
+
+// |p - j|, exact in 32 bits for any two positions
+__device__ __forceinline__ float distance(int p, int j) {
+  return static_cast<float>(p > j ? static_cast<unsigned>(p) - j : static_cast<unsigned>(j) - p);
 }
 
 // tanh(y) = 1 - 2 / (1 + e^2y): within about 2e-7 absolute, which the cap scales
@@ -239,10 +246,10 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   const int rt = blockIdx.x % p.row_tiles, split = blockIdx.x / p.row_tiles;
   const int hkv = blockIdx.y, b = blockIdx.z;
   const int ps = p.pool.page_size;
-  const SeqView s = seq_view(p.batch, b, ps);
+  const SeqView s = seq_view(p.batch, b);
   const int rows = s.nq * p.group, r0 = rt * ROWS;
   if (r0 >= rows) return;
-  long long p_lo, p_hi;
+  int p_lo, p_hi;
   unit_positions(p, s, r0, p_lo, p_hi);
   const KeyRange kr = key_range(p.sc, b, s, p_lo, p_hi, 16);
   const int pieces = piece_count(p, kr.nt);
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     if (k < n_my) {
       if ((k & 31) == 0) {  // the pages of this warp's next 32 tiles, one per lane
         const int kk = k + lane;
-        my_page = kk < n_my ? page_of(p.batch, b, kr.tile(t_beg + kk * NW) * 16 / ps, p.pool.n_pages) : -1;
+        my_page = kk < n_my ? page_of(p.batch, b, kr.tile(t_beg + kk * NW) * 16 >> p.pool.page_shift, p.pool.n_pages) : -1;
       }
       const int page = __shfl_sync(0xffffffffu, my_page, k & 31);
       const int key0 = kr.tile(t_beg + k * NW) * 16;
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     for (int q = 0; q < 2; ++q) {
       const int row = 2 * t + q + 8 * r;
       fac[2 * r + q] = s_qf[row] * p.sc.pre;
-      pos[2 * r + q] = static_cast<int>(max(s.first_pos + (r0 + row) / p.group, -(1ll << 30)));
+      pos[2 * r + q] = s.first_pos + (r0 + row) / p.group;
       slope[2 * r + q] = MODS && p.sc.biased ? p.sc.slope2[hkv * p.group + (r0 + row) % p.group] : 0.f;
     }
   }
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
         sx[r][e] = MODS ? score2(p.sc, y, f) : y * f;
         if (MODS && p.sc.biased) {
           const int j = key0 + g + 8 * (e >> 1);
-          sx[r][e] -= slope[2 * r + (e & 1)] * fabsf(static_cast<float>(pos[2 * r + (e & 1)] - j));
+          sx[r][e] -= slope[2 * r + (e & 1)] * distance(pos[2 * r + (e & 1)], j);
         }
       }
     const bool all_seen = mt.z != 0.f && (key0 + 16 <= kr.prefix ||
@@ -608,13 +615,13 @@ constexpr int kJoinThreads = 128;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnParams p) {
   const int b = blockIdx.y;
-  const SeqView s = seq_view(p.batch, b, p.pool.page_size);
+  const SeqView s = seq_view(p.batch, b);
   const int w = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int tok = w / p.Hq, h = w - tok * p.Hq;
   int pieces = 1;
   if (tok < s.nq) {
     const int row = tok * p.group + h % p.group;
-    long long lo, hi;
+    int lo, hi;
     unit_positions(p, s, row / p.row_tile * p.row_tile, lo, hi);
     pieces = piece_count(p, key_range(p.sc, b, s, lo, hi, p.key_tile).nt);
   }

@@ -64,8 +64,8 @@ struct KeyGroup {
 
 // Like turn_of, with the hardware's sine and cosine of at most an eighth of a
 // turn (within 2^-21): for queries, which are rounded to 16 bits right after.
-__device__ __forceinline__ float2 turn_fast(const TokenRope& r, long long pos, int i) {
-  const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * r.turns[i]) >> 32);
+__device__ __forceinline__ float2 turn_fast(const TokenRope& r, int pos, int i) {
+  const uint32_t t = turned(pos, r.turns[i]);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
   const float a = static_cast<float>(static_cast<int>(t - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
   float s, c;
@@ -125,10 +125,10 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
   const int rt = p.row_tiles - 1 - blockIdx.x % p.row_tiles, split = blockIdx.x / p.row_tiles;
   const int hkv = blockIdx.y, b = blockIdx.z;
   const int ps = p.pool.page_size;
-  const SeqView s = seq_view(p.batch, b, ps);
+  const SeqView s = seq_view(p.batch, b);
   const int rows = s.nq * p.group, r0 = rt * 2 * BM;
   if (r0 >= rows) return;
-  long long p_lo, p_hi;
+  int p_lo, p_hi;
   unit_positions(p, s, r0, p_lo, p_hi);
   const KeyRange kr = key_range(p.sc, b, s, p_lo, p_hi, BN);
   const int pieces = piece_count(p, kr.nt);
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
     auto page_for = [&](int i) -> int {
       if (lane >= 8 || i >= n) return -1;
       const int key = kr.tile(t_beg + i) * BN + lane * 16;
-      return key < s.len ? page_of(p.batch, b, key / ps, p.pool.n_pages) : -1;
+      return key < s.len ? page_of(p.batch, b, key >> p.pool.page_shift, p.pool.n_pages) : -1;
     };
     auto run_of = [&](int i, int page) -> int {
       return page < 0 ? -1 : (page * p.pool.H + hkv) * per_page + ((kr.tile(t_beg + i) * 8 + lane) & (per_page - 1));
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
     const bool live = ur < rows;
     if (w == 0 || two) {
       const int tok = ur / p.group, h = hkv * p.group + ur % p.group;
-      const long long pos = s.first_pos + tok;
+      const int pos = s.first_pos + tok;
       // ---- this row of Q, rotated, into the operand layout
       float qf = 1.f;
       {
@@ -480,16 +480,14 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       // ---- the keys this row sees: [0, sees_a) and [sees_b, sees_e)
       int sees_a = 0, sees_b = 0, sees_e = 0;
       if (live) {
-        const long long e = pos + 1 < s.len ? pos + 1 : s.len;
-        sees_e = static_cast<int>(e > 0 ? e : 0);
-        const long long lo = p.sc.window > 0 ? pos - p.sc.window + 1 : 0;
-        sees_b = static_cast<int>(lo < 0 ? 0 : (lo < sees_e ? lo : sees_e));
+        sees_e = max(min(pos + 1, s.len), 0);
+        sees_b = min(window_begin(p.sc, pos), sees_e);
         const int sink = p.sc.window > 0 ? min(p.sc.n_sink, sees_e) : 0;
         sees_a = max(kr.prefix, sink);
       }
       // positions of this tile's first and last row, for tiles that need no mask
-      const long long w_lo = s.first_pos + (r0 + w * BM) / p.group;
-      const long long w_hi = s.first_pos + (min(r0 + w * BM + BM, rows) - 1) / p.group;
+      const int w_lo = s.first_pos + (r0 + w * BM) / p.group;
+      const int w_hi = s.first_pos + (min(r0 + w * BM + BM, rows) - 1) / p.group;
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tS = tbase + lane_off + TR::S_COL + w * BN;
       const uint32_t tO = tbase + lane_off + TR::O_COL + w * D;
@@ -516,13 +514,12 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
                                                 (key0 + TR::HN - 1 <= w_lo && key0 + TR::HN <= s.len &&
                                                  (p.sc.window == 0 || w_hi - key0 < p.sc.window)));
         if constexpr (MODS) {
-          const float pj = static_cast<float>(pos - key0);
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               float x = score2(p.sc, __uint_as_float(sr[c][e]), E4M3 ? fac * kg[2 * c + (e >> 4)].ks : fac);
-              x -= slope * fabsf(pj - static_cast<float>(c * 32 + e));
+              x -= slope * distance(pos, key0 + c * 32 + e);
               sr[c][e] = __float_as_uint(x);
             }
         }

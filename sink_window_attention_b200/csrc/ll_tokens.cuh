@@ -16,30 +16,26 @@ struct TokenBatch {
   const int* q_start;
   const int* kv_len;
   const int* page_table;
-  int B, max_pages, total_q, max_q, max_kv;
+  int B, max_pages, total_q, max_q;
+  int max_key;  // keys that may exist: min(max_kv, max_pages * page_size, 2^31 - 257)
 };
 
-// Sequence b with everything the device arrays say brought within bounds.
+// Sequence b with everything the device arrays say brought within bounds (32-bit
+// throughout: positions lie in (-2^31, 2^31 - 1)).
 struct SeqView {
-  int q0, nq;           // rows [q0, q0 + nq) of the token tensors are processed
-  long long first_pos;  // position of row q0 (may be negative: such rows stand before the first key)
-  int len;              // keys [0, len) exist
+  int q0, nq;     // rows [q0, q0 + nq) of the token tensors are processed
+  int first_pos;  // position of row q0 (may be negative: such rows stand before the first key)
+  int len;        // keys [0, len) exist
 };
 
-__device__ __forceinline__ SeqView seq_view(const TokenBatch& t, int b, int page_size) {
+__device__ __forceinline__ SeqView seq_view(const TokenBatch& t, int b) {
+  const int a = t.q_start[b], e = t.q_start[b + 1], kv = max(t.kv_len[b], 0);
   SeqView s;
-  const long long a = t.q_start[b], e = t.q_start[b + 1], kv = t.kv_len[b];
-  const long long rows = e > a ? e - a : 0;
-  s.q0 = static_cast<int>(a < 0 ? 0 : (a > t.total_q ? t.total_q : a));
-  s.first_pos = kv - rows + (s.q0 - a);
-  long long n = rows - (s.q0 - a);
-  n = n < t.max_q ? n : t.max_q;
-  n = n < t.total_q - s.q0 ? n : t.total_q - s.q0;
-  s.nq = static_cast<int>(n > 0 ? n : 0);
-  const long long cap = static_cast<long long>(t.max_pages) * page_size;
-  long long len = kv < t.max_kv ? kv : t.max_kv;
-  len = len < cap ? len : cap;
-  s.len = static_cast<int>(len > 0 ? len : 0);
+  s.q0 = min(max(a, 0), t.total_q);
+  const int rows = max(e, s.q0) - s.q0;
+  s.first_pos = kv - rows;
+  s.nq = min(min(rows, t.max_q), t.total_q - s.q0);
+  s.len = min(kv, t.max_key);
   return s;
 }
 
@@ -62,21 +58,33 @@ struct TokenRope {
   unsigned long long turns[kMaxTokenPairs];
 };
 
-// (cos, sin) of a pair at position `pos`, times the amplitude. The angle in turns is
-// pos * turn modulo 2^64: exact, so a far position costs no accuracy (a
-// product of an fp32 position and frequency would be off by 0.03 rad at
-// position 10^6). The nearest quarter turn is taken off in integers, so the rest
-// (at most an eighth of a turn) keeps all of fp32's bits.
-__device__ __forceinline__ float2 turn_of(const TokenRope& r, long long pos, unsigned long long turn) {
-  const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * turn) >> 32);
+// The angle of position `pos` in units of 2^-32 turns: the upper half of pos * turn
+// modulo 2^64. Exact but for the 2^-32 cut off, so a far position costs no accuracy (a
+// product of an fp32 position and frequency would be off by 0.03 rad at position 10^6).
+__device__ __forceinline__ uint32_t turned(int pos, unsigned long long turn) {
+  const uint32_t p = static_cast<uint32_t>(pos), lo = static_cast<uint32_t>(turn), hi = static_cast<uint32_t>(turn >> 32);
+  return __umulhi(p, lo) + p * hi - (pos < 0 ? lo : 0u);  // p is pos + 2^32 where pos < 0
+}
+
+// (cos, sin) of that angle, times the amplitude. The nearest quarter turn is taken off
+// in integers, so the rest (at most an eighth of a turn, y <= pi / 4) keeps all of
+// fp32's bits; there the Taylor polynomials to y^9 and y^10 are within 2e-9.
+__device__ __forceinline__ float2 turn_of(const TokenRope& r, int pos, unsigned long long turn) {
+  const uint32_t t = turned(pos, turn);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
-  const float a = static_cast<float>(static_cast<int>(t - (quarter << 30))) * 4.656612873077393e-10f;  // half turns
-  float s, c;
-  sincospif(a, &s, &c);
-  float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
-  if ((quarter + 1) & 2) x = -x;  // quarters 1 and 2
-  if (quarter & 2) y = -y;        // quarters 2 and 3
-  return make_float2(x * r.amp, y * r.amp * r.sign);
+  const float y = static_cast<float>(static_cast<int>(t - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = y * y;
+  float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+  s = fmaf(z, s, 1.f / 120.f);
+  s = fmaf(z, s, -1.f / 6.f);
+  s = fmaf(y * z, s, y);
+  float c = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+  c = fmaf(z, c, -1.f / 720.f);
+  c = fmaf(z, c, 1.f / 24.f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.f);
+  const float u = (quarter & 1 ? s : c) * r.amp, v = (quarter & 1 ? c : s) * (r.amp * r.sign);
+  return make_float2((quarter + 1) & 2 ? -u : u, quarter & 2 ? -v : v);  // quarters 1, 2; quarters 2, 3
 }
 
 // The unit that the rotating kernels work in: 16 elements of a head, pairs
@@ -141,10 +149,10 @@ __device__ __forceinline__ TurnTable make_turn_table(const TokenRope& r, float2*
   TurnTable tab{cs, r.rot >> 1, r.rot >> 4};
   for (int i = threadIdx.x; i < tab.pairs; i += blockDim.x) s_turns[i] = r.turns[i];
   __syncthreads();
-  for (int i = threadIdx.x; i < nt * tab.pairs; i += blockDim.x) {
-    const int t = i / tab.pairs, j = i - t * tab.pairs;  // entry j of the row: pair 8 (j % step) + j / step
-    const int e = j / tab.step, c = j - e * tab.step;
-    cs[t * (tab.pairs + 8) + j] = turn_of(r, position_of(t), s_turns[c * 8 + e]);
+  for (int t = threadIdx.x >> 5; t < nt; t += blockDim.x >> 5) {
+    const int pos = position_of(t);
+    for (int i = threadIdx.x & 31; i < tab.pairs; i += 32)
+      cs[t * (tab.pairs + 8) + (i & 7) * tab.step + (i >> 3)] = turn_of(r, pos, s_turns[i]);
   }
   __syncthreads();
   return tab;
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(kTokenRopeThreads) token_rope_kernel(const Tok
   extern __shared__ float2 s_cs[];
   const int t0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, p.T - t0);
-  const TurnTable tab = make_turn_table(p.rope, s_cs, nt, [&](int t) { return static_cast<long long>(p.positions[t0 + t]); });
+  const TurnTable tab = make_turn_table(p.rope, s_cs, nt, [&](int t) { return p.positions[t0 + t]; });
   const int per_head = p.D >> 4, per_token = p.H * per_head;
   const int items = nt * per_token;
   for (int i = threadIdx.x; i < items; i += blockDim.x) {
@@ -197,7 +205,7 @@ struct PagedPool {
   void* v;
   float* k_scale;
   float* v_scale;
-  int n_pages, page_size, H, D;
+  int n_pages, page_size, page_shift, H, D;  // page_size = 1 << page_shift
 };
 
 struct PagedAppendParams {
@@ -218,7 +226,7 @@ constexpr int kPagedAppendMaxThreads = 1024;  // 8-bit pool: a thread per 16 ele
 __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_bf16_kernel(const PagedAppendParams p) {
   extern __shared__ float2 s_cs[];
   const int b = blockIdx.y;
-  const SeqView s = seq_view(p.batch, b, p.pool.page_size);
+  const SeqView s = seq_view(p.batch, b);
   const int i0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, s.nq - i0);
   if (nt <= 0) return;
@@ -228,13 +236,13 @@ __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_bf16_kernel(
   for (int i = threadIdx.x; i < nt * per_token; i += blockDim.x) {
     const int t = i / per_token, r = i - t * per_token;
     const int h = r / per_head, c = r - h * per_head;
-    const long long pos = s.first_pos + i0 + t;
-    if (pos < 0 || pos >= static_cast<long long>(p.batch.max_pages) * ps) continue;
-    const int page = page_of(p.batch, b, static_cast<int>(pos / ps), p.pool.n_pages);
+    const int pos = s.first_pos + i0 + t;
+    if (pos < 0 || pos >> p.pool.page_shift >= p.batch.max_pages) continue;
+    const int page = page_of(p.batch, b, pos >> p.pool.page_shift, p.pool.n_pages);
     if (page < 0) continue;
     int lo, hi;
     item_chunks(p.rope, c, lo, hi);
-    const long long row = s.q0 + i0 + t;
+    const size_t row = s.q0 + i0 + t;
     const __nv_bfloat16* kr = p.k + row * p.k_stride + h * D;
     const __nv_bfloat16* vr = p.v + row * p.v_stride + h * D;
     const uint4 v0 = *reinterpret_cast<const uint4*>(vr + lo * 8), v1 = *reinterpret_cast<const uint4*>(vr + hi * 8);
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_bf16_kernel(
     load_chunk8<__nv_bfloat16>(kr + lo * 8, x);
     load_chunk8<__nv_bfloat16>(kr + hi * 8, y);
     if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x, y, tab.unit(t, c), tab.step);
-    const size_t at = ((static_cast<size_t>(page) * H + h) * ps + static_cast<int>(pos % ps)) * D;
+    const size_t at = ((static_cast<size_t>(page) * H + h) * ps + (pos & (ps - 1))) * D;
     __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(p.pool.k) + at;
     __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.pool.v) + at;
     store_chunk8<__nv_bfloat16>(kd + lo * 8, x);
@@ -261,17 +269,26 @@ __device__ __forceinline__ float two_power_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e < 1 ? 1 : e) << 23);
 }
 
+// |x|, 0 for an infinity or NaN
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;  // infinity and NaN do not set a scale
+  return a <= 3.402823466e38f ? a : 0.f;
 }
 
+// E4M3 codes of x * inv: to nearest even, saturating at +-448 (NaN stays NaN).
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(w)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return w;
+}
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  return make_uint2(encode4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                    encode4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
 __device__ __forceinline__ uint2 recode8(uint2 c, float ratio) {
@@ -298,15 +315,11 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
   }
 }
 
-// The largest finite |x| of eight bf16 values: as integers, where an exponent of all
-// ones (infinity, NaN) counts as 0.
-__device__ __forceinline__ uint32_t bf16_amax(const uint4& u, uint32_t a) {
+// The largest |x| of eight bf16 values, NaN left out.
+__device__ __forceinline__ __nv_bfloat162 bf16_amax(const uint4& u, __nv_bfloat162 a) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] << 16 & 0x7FFF0000u, hi = w[i] & 0x7FFF0000u;
-    a = max(a, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
-  }
+  for (int i = 0; i < 4; ++i) a = __hmax2(a, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
   return a;
 }
 
@@ -321,15 +334,13 @@ __global__ void __launch_bounds__(kPagedAppendMaxThreads, 1) paged_append_e4m3_k
   extern __shared__ float2 s_cs[];
   __shared__ uint32_t s_max[2][2][kPagedAppendMaxThreads / 32];  // [parity][K, V][warp]: bits of the maximum
   const int b = blockIdx.y, ps = p.pool.page_size, D = p.pool.D, H = p.pool.H;
-  const SeqView s = seq_view(p.batch, b, ps);
+  const SeqView s = seq_view(p.batch, b);
   // page number within the sequence, and the rows of it that are new
-  const long long beg = s.first_pos > 0 ? s.first_pos : 0;
-  const long long end = s.first_pos + s.nq;
-  const long long pg = beg / ps + blockIdx.x;
-  if (pg * ps >= end || pg >= p.batch.max_pages) return;
-  const int n0 = static_cast<int>((beg > pg * ps ? beg : pg * ps) - pg * ps);
-  const int n1 = static_cast<int>((end < (pg + 1) * ps ? end : (pg + 1) * ps) - pg * ps);
-  const int page = page_of(p.batch, b, static_cast<int>(pg), p.pool.n_pages);
+  const int beg = max(s.first_pos, 0), end = s.first_pos + s.nq;
+  const int pg = (beg >> p.pool.page_shift) + blockIdx.x;
+  if (pg >= p.batch.max_pages || pg > (end - 1) >> p.pool.page_shift || end <= beg) return;
+  const int n0 = max(beg - pg * ps, 0), n1 = min(end - pg * ps, ps);
+  const int page = page_of(p.batch, b, pg, p.pool.n_pages);
   if (page < 0) return;
   const int per_head = D >> 4;
   const int units = ps * per_head;  // of a head: a multiple of 32, so a warp holds one head
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(kPagedAppendMaxThreads, 1) paged_append_e4m3_k
   item_chunks(p.rope, c, lo, hi);
   const bool fresh = slot >= n0 && slot < n1;
   const int h_end = min(H, static_cast<int>(blockIdx.z + 1) * p.heads);
-  const long long row = s.q0 + (pg * ps - s.first_pos) + slot;  // of the token tensors
+  const int row = s.q0 + (pg * ps - s.first_pos) + slot;  // of the token tensors, where fresh
   const __nv_bfloat16* kr = p.k + row * p.k_stride;
   const __nv_bfloat16* vr = p.v + row * p.v_stride;
   uint4 raw[4];  // K lo, K hi, V lo, V hi
@@ -370,11 +381,25 @@ __global__ void __launch_bounds__(kPagedAppendMaxThreads, 1) paged_append_e4m3_k
       unpack8(raw[0], x);
       unpack8(raw[1], y);
       if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x, y, tab.unit(slot - n0, c), tab.step);
+      // an infinity shows in the maximum (NaN never does): only then it is looked for
       float a = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a = fmax3(a, finite_abs(x[e]), finite_abs(y[e]));
+      for (int e = 0; e < 8; ++e) a = fmax3(a, fabsf(x[e]), fabsf(y[e]));
+      const __nv_bfloat162 vm = bf16_amax(v1, bf16_amax(v0, __floats2bfloat162_rn(0.f, 0.f)));
+      float av = fmaxf(__low2float(vm), __high2float(vm));
+      if (fmaxf(a, av) > 3.402823466e38f) {
+        float z[8], q[8];
+        unpack8(v0, z);
+        unpack8(v1, q);
+        a = av = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a = fmax3(a, finite_abs(x[e]), finite_abs(y[e]));
+          av = fmax3(av, finite_abs(z[e]), finite_abs(q[e]));
+        }
+      }
       amax[0] = __float_as_uint(a);
-      amax[1] = bf16_amax(v1, bf16_amax(v0, 0u));
+      amax[1] = __float_as_uint(av);
     }
     load(h + side);
 #pragma unroll
@@ -383,12 +408,13 @@ __global__ void __launch_bounds__(kPagedAppendMaxThreads, 1) paged_append_e4m3_k
       if ((threadIdx.x & 31) == 0) s_max[parity][w][threadIdx.x >> 5] = amax[w];
     }
     __syncthreads();  // one per round: the next round writes the other parity
-    if (!live) continue;
+    if (!live) continue;  // a whole warp
     float scale[2], inv[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      uint32_t m = 0u;
-      for (int i = slot_h * (units >> 5); i < (slot_h + 1) * (units >> 5); ++i) m = max(m, s_max[parity][w][i]);
+      const int lane = threadIdx.x & 31;  // of the head's warps (at most 32), one each
+      const uint32_t m =
+          __reduce_max_sync(0xffffffffu, lane < units >> 5 ? s_max[parity][w][slot_h * (units >> 5) + lane] : 0u);
       scale[w] = fmaxf(was[w], two_power_scale(__uint_as_float(m)));
       inv[w] = scale[w] > 0.f ? 1.0f / scale[w] : 0.f;
     }
