@@ -182,7 +182,7 @@ size_t paged_workspace(const AttnPlan& a, const ll_token_batch* t, int Hq, int D
          align256(static_cast<size_t>(t->total_q) * Hq * a.nsplit * sizeof(float2));
 }
 
-template <class TR, bool MODS>
+template <class TR, int MODS>
 ll_status launch_paged_decode(const ll::PagedAttnParams& p, cudaStream_t s) {
   auto kern = ll::paged_decode_kernel<TR, MODS>;
   static std::atomic<unsigned long long> done{0};
@@ -192,7 +192,7 @@ ll_status launch_paged_decode(const ll::PagedAttnParams& p, cudaStream_t s) {
   return check_launch("paged_decode_kernel");
 }
 
-template <class TR, bool MODS>
+template <class TR, int MODS>
 ll_status launch_paged_prefill(const ll::PagedAttnParams& p, cudaStream_t s) {
   auto kern = ll::paged_prefill_kernel<TR, MODS>;
   static std::atomic<unsigned long long> done{0};
@@ -202,19 +202,20 @@ ll_status launch_paged_prefill(const ll::PagedAttnParams& p, cudaStream_t s) {
   return check_launch("paged_prefill_kernel");
 }
 
+template <int D, bool E4M3, int MODS>
+ll_status launch_paged(const AttnPlan& plan, const ll::PagedAttnParams& p, cudaStream_t s) {
+  if (plan.tiles) return launch_paged_prefill<ll::PrefillTraits<D, E4M3>, MODS>(p, s);
+  return plan.row_tile == 8 ? launch_paged_decode<ll::DecodeTraits<D, E4M3, 8>, MODS>(p, s)
+                            : launch_paged_decode<ll::DecodeTraits<D, E4M3, 16>, MODS>(p, s);
+}
+
 template <int D, bool E4M3>
 ll_status launch_paged(const AttnPlan& plan, const ll::PagedAttnParams& p, cudaStream_t s) {
-  const bool mods = p.sc.cap2 > 0.f || p.sc.biased;  // scores are more than a scaled product
-  if (!plan.tiles) {
-    if (plan.row_tile == 8) {
-      using TR = ll::DecodeTraits<D, E4M3, 8>;
-      return mods ? launch_paged_decode<TR, true>(p, s) : launch_paged_decode<TR, false>(p, s);
-    }
-    using TR = ll::DecodeTraits<D, E4M3, 16>;
-    return mods ? launch_paged_decode<TR, true>(p, s) : launch_paged_decode<TR, false>(p, s);
-  }
-  using TR = ll::PrefillTraits<D, E4M3>;
-  return mods ? launch_paged_prefill<TR, true>(p, s) : launch_paged_prefill<TR, false>(p, s);
+  const bool capped = p.sc.cap2 > 0.f, biased = p.sc.biased != 0;
+  if (capped && biased) return launch_paged<D, E4M3, ll::kCapped | ll::kBiased>(plan, p, s);
+  if (capped) return launch_paged<D, E4M3, ll::kCapped>(plan, p, s);
+  if (biased) return launch_paged<D, E4M3, ll::kBiased>(plan, p, s);
+  return launch_paged<D, E4M3, 0>(plan, p, s);
 }
 
 // The join starts while the pieces' kernel drains and waits for its end on the

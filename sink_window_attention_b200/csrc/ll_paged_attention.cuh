@@ -92,9 +92,13 @@ __device__ __forceinline__ int piece_count(const PagedAttnParams& p, int nt) {
   return n > 1 ? n : 1;
 }
 
-// |p - j|, exact in 32 bits for any two positions
-__device__ __forceinline__ float distance(int p, int j) {
-  return static_cast<float>(p > j ? static_cast<unsigned>(p) - j : static_cast<unsigned>(j) - p);
+// What a kernel is compiled for beyond a scaled product: a branch per score, or the
+// cap's exponential in calls that have none, would cost more than a copy of the code.
+enum : int { kCapped = 1, kBiased = 2 };
+
+// p - j, for a bias: exact where it matters (below 2^24), never overflowing.
+__device__ __forceinline__ float offset_of(int p, int j) {
+  return p >= j ? static_cast<float>(static_cast<unsigned>(p) - j) : -static_cast<float>(static_cast<unsigned>(j) - p);
 }
 
 // tanh(y) = 1 - 2 / (1 + e^2y): within about 2e-7 absolute, which the cap scales
@@ -103,10 +107,13 @@ __device__ __forceinline__ float tanh_accurate(float y) {
   return 1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * y));
 }
 
-// The score in log2 units from s = q.k.
-__device__ __forceinline__ float score2(const ScoreParams& sc, float s, float factor) {
-  const float y = s * factor;
-  return sc.cap2 > 0.f ? sc.cap2 * tanh_accurate(y) : y;
+// The score in log2 units from s = q.k; away: p - j.
+template <int MODS>
+__device__ __forceinline__ float score2(const ScoreParams& sc, float s, float factor, float slope, float away) {
+  float y = s * factor;
+  if constexpr ((MODS & kCapped) != 0) y = sc.cap2 * tanh_accurate(y);
+  if constexpr ((MODS & kBiased) != 0) y = fmaf(-slope, fabsf(away), y);
+  return y;
 }
 
 // The power of two 2^e with 2^e <= a < 2^(e+1), kept within [2^-125, 2^126] (1 for 0).
@@ -229,7 +236,7 @@ __device__ __forceinline__ int swz(int row, int c) {
   return c ^ ((((row ^ (row >> 2)) & 1) << 2) | (row & 2));
 }
 
-template <class TR, bool MODS>
+template <class TR, int MODS>
 __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(const PagedAttnParams p) {
   constexpr int D = TR::D, CH = TR::CH, NW = TR::NW, STAGES = TR::STAGES, TILE = TR::TILE;
   constexpr int ROWS = TR::ROWS, NR = TR::NR, MT = TR::MT;
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
       const int row = 2 * t + q + 8 * r;
       fac[2 * r + q] = s_qf[row] * p.sc.pre;
       pos[2 * r + q] = s.first_pos + (r0 + row) / p.group;
-      slope[2 * r + q] = MODS && p.sc.biased ? p.sc.slope2[hkv * p.group + (r0 + row) % p.group] : 0.f;
+      slope[2 * r + q] = MODS & kBiased ? p.sc.slope2[hkv * p.group + (r0 + row) % p.group] : 0.f;
     }
   }
 
@@ -442,11 +449,8 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float f = fac[2 * r + (e & 1)] * ks, y = sx[r][e] + sy[r][e];
-        sx[r][e] = MODS ? score2(p.sc, y, f) : y * f;
-        if (MODS && p.sc.biased) {
-          const int j = key0 + g + 8 * (e >> 1);
-          sx[r][e] -= slope[2 * r + (e & 1)] * distance(pos[2 * r + (e & 1)], j);
-        }
+        const int q = 2 * r + (e & 1);
+        sx[r][e] = score2<MODS>(p.sc, y, f, slope[q], MODS & kBiased ? offset_of(pos[q], key0 + g + 8 * (e >> 1)) : 0.f);
       }
     const bool all_seen = mt.z != 0.f && (key0 + 16 <= kr.prefix ||
                                           (key0 + 15 <= p_lo && key0 + 16 <= s.len &&

@@ -94,7 +94,7 @@ __device__ __forceinline__ bool mbar_wait_sleeping(uint64_t* bar, uint32_t parit
   return true;
 }
 
-template <class TR, bool MODS>
+template <class TR, int MODS>
 __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const PagedAttnParams p) {
   constexpr int D = TR::D, BM = TR::BM, BN = TR::BN, STAGES = TR::STAGES, TILE = TR::TILE;
   constexpr bool E4M3 = TR::E4M3;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       const uint32_t tS = tbase + lane_off + TR::S_COL + w * BN;
       const uint32_t tO = tbase + lane_off + TR::O_COL + w * D;
       const float fac = qf * p.sc.pre;
-      const float slope = MODS && p.sc.biased ? p.sc.slope2[h] : 0.f;
+      const float slope = MODS & kBiased ? p.sc.slope2[h] : 0.f;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < 2 * n; ++j) {  // halves of key tiles
@@ -513,15 +513,15 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         const bool all_seen = mapped == 15u && (key0 + TR::HN <= kr.prefix ||
                                                 (key0 + TR::HN - 1 <= w_lo && key0 + TR::HN <= s.len &&
                                                  (p.sc.window == 0 || w_hi - key0 < p.sc.window)));
-        if constexpr (MODS) {
+        if constexpr (MODS != 0) {
+          const float away = MODS & kBiased ? offset_of(pos, key0) : 0.f;  // of key 0 of the half
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float x = score2(p.sc, __uint_as_float(sr[c][e]), E4M3 ? fac * kg[2 * c + (e >> 4)].ks : fac);
-              x -= slope * distance(pos, key0 + c * 32 + e);
-              sr[c][e] = __float_as_uint(x);
-            }
+            for (int e = 0; e < 32; ++e)
+              sr[c][e] = __float_as_uint(score2<MODS>(p.sc, __uint_as_float(sr[c][e]),
+                                                      E4M3 ? fac * kg[2 * c + (e >> 4)].ks : fac, slope,
+                                                      away - static_cast<float>(c * 32 + e)));
         }
         if (!all_seen) {
           const int a = sees_a - key0, bb = sees_b - key0, ee = sees_e - key0;
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
             }
         }
         // factor on the scores of group g (kept off 0, so that masked ones stay -inf)
-        auto factor = [&](int g) { return MODS ? 1.f : (E4M3 ? fmaxf(fac * kg[g].ks, 1e-37f) : fac); };
+        auto factor = [&](int g) { return MODS != 0 ? 1.f : (E4M3 ? fmaxf(fac * kg[g].ks, 1e-37f) : fac); };
         float mx = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
