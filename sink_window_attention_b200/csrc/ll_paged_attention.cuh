@@ -38,6 +38,7 @@ struct PagedAttnParams {
   int key_tile;      // keys per step; pieces begin at multiples of it
   int chunk;         // key tiles per piece
   int nsplit;        // pieces at most
+  int clustered;     // decode: the nsplit blocks of a unit form a cluster, share its keys evenly and join on chip
   int row_tiles;     // units of a sequence and K/V head at most
   float* part_o;     // [total_q][Hq][nsplit][D], unnormalised
   float2* part_ml;   // [total_q][Hq][nsplit]: (max, sum), max in log2 units
@@ -227,8 +228,29 @@ struct DecodeTraits {
   static constexpr int BLOCKS = ROWB >= 256 ? 2 : (ROWS == 8 ? 4 : 3);
   static constexpr int META = NW * STAGES * 16;
   static constexpr int SMEM = RING + META + ROWS * QP * 2 + ROWS * 4 + 2 * NW * ROWS * 4;
-  static_assert(NW * ROWS * D * 4 <= RING, "the warps' O must fit the ring");
+  static_assert((NW + 1) * ROWS * D * 4 <= RING, "the warps' O and their sum must fit the ring");
 };
+
+// All threads of all blocks of the cluster; orders their shared memory accesses.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same place in the shared memory of block `rank` of the cluster.
+template <class T>
+__device__ __forceinline__ const T* cluster_ptr(const T* p, int rank) {
+  uint64_t q;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<const T*>(q);
+}
+
+// Four elements of a finished row: O / L (a row that saw no key: 0), and its lse.
+__device__ __forceinline__ void store_row(const PagedAttnParams& p, size_t at, int d4, int D, const float4& a, float M,
+                                          float L) {
+  const float inv = M == -INFINITY ? 0.f : 1.f / L;
+  *reinterpret_cast<uint2*>(p.out + at * D + d4 * 4) =
+      make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+  if (p.lse != nullptr && d4 == 0) p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
 
 template <int CH>
 __device__ __forceinline__ int swz(int row, int c) {
@@ -250,20 +272,21 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   float* s_l = s_m + NW * ROWS;
 
   asm volatile("griddepcontrol.launch_dependents;");
-  const int rt = blockIdx.x % p.row_tiles, split = blockIdx.x / p.row_tiles;
+  const int split = blockIdx.x % p.nsplit, rt = blockIdx.x / p.nsplit;
   const int hkv = blockIdx.y, b = blockIdx.z;
   const int ps = p.pool.page_size;
   const SeqView s = seq_view(p.batch, b);
   const int rows = s.nq * p.group, r0 = rt * ROWS;
-  if (r0 >= rows) return;
+  if (r0 >= rows) return;  // all blocks of the cluster
   int p_lo, p_hi;
   unit_positions(p, s, r0, p_lo, p_hi);
   const KeyRange kr = key_range(p.sc, b, s, p_lo, p_hi, 16);
-  const int pieces = piece_count(p, kr.nt);
+  const int pieces = p.clustered ? p.nsplit : piece_count(p, kr.nt);
   if (split >= pieces) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t_beg = split * p.chunk + warp;
-  const int t_end = min(kr.nt, (split + 1) * p.chunk);
+  const int chunk = p.clustered ? (kr.nt + pieces - 1) / pieces : p.chunk;
+  const int t_beg = split * chunk + warp;
+  const int t_end = min(kr.nt, (split + 1) * chunk);
   const int n_my = t_end > t_beg ? (t_end - t_beg + NW - 1) / NW : 0;
 
   // ---- the ring
@@ -562,6 +585,8 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     }
   __syncthreads();
   float* s_o = reinterpret_cast<float*>(s_ring);  // [NW][ROWS][D]
+  float* c_o = s_o + NW * ROWS * D;               // [ROWS][D]: the block's sum, for its cluster
+  float2* c_ml = reinterpret_cast<float2*>(s_q);  // [ROWS]
 #pragma unroll
   for (int q = 0; q < 2 * NR; ++q) {
     const int row = 2 * t + (q & 1) + 8 * (q >> 1);
@@ -598,30 +623,60 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     }
     const size_t at = static_cast<size_t>(s.q0 + row / p.group) * p.Hq + hkv * p.group + row % p.group;
     if (pieces == 1) {
-      const float inv = M == -INFINITY ? 0.f : 1.f / L;
-      *reinterpret_cast<uint2*>(p.out + at * D + d4 * 4) =
-          make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-      if (p.lse != nullptr && d4 == 0) p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      store_row(p, at, d4, D, a, M, L);
+    } else if (p.clustered) {
+      *reinterpret_cast<float4*>(c_o + r * D + d4 * 4) = a;
+      if (d4 == 0) c_ml[r] = make_float2(M, L);
     } else {
       __stcg(reinterpret_cast<float4*>(p.part_o + (at * p.nsplit + split) * D + d4 * 4), a);
       if (d4 == 0) __stcg(p.part_ml + at * p.nsplit + split, make_float2(M, L));
     }
   }
+  if (p.clustered && pieces > 1) {
+    // the cluster's blocks join their rows through each other's shared memory, a share
+    // of the elements each
+    cluster_barrier();
+    for (int i = threadIdx.x + split * TR::THREADS; i < ROWS * (D / 4); i += pieces * TR::THREADS) {
+      const int r = i / (D / 4), d4 = i % (D / 4);
+      const int row = r0 + r;
+      if (row >= rows) break;
+      float M = -INFINITY, L = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < pieces; ++c) {
+        const float2 ml = *reinterpret_cast<const float2*>(cluster_ptr(c_ml + r, c));
+        const float4 u = *reinterpret_cast<const float4*>(cluster_ptr(c_o + r * D + d4 * 4, c));
+        const float nm = fmaxf(M, ml.x);
+        const float f0 = M == -INFINITY ? 0.f : ex2(M - nm), f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - nm);
+        M = nm;
+        L = L * f0 + ml.y * f1;
+        a.x = a.x * f0 + u.x * f1;
+        a.y = a.y * f0 + u.y * f1;
+        a.z = a.z * f0 + u.z * f1;
+        a.w = a.w * f0 + u.w * f1;
+      }
+      const size_t at = static_cast<size_t>(s.q0 + row / p.group) * p.Hq + hkv * p.group + row % p.group;
+      store_row(p, at, d4, D, a, M, L);
+    }
+    cluster_barrier();  // nobody leaves while its shared memory is read
+  }
 }
 
 // ---------------------------------------------------------------------------
-// Joins the pieces of every row whose key range was split: one warp per (row,
-// query head). Launched behind the kernel that wrote them, whose end it awaits
-// on the device (programmatic dependent launch).
+// Joins the pieces of every row whose key range was split: one block per (row, query
+// head), its warps taking pieces in turn. Launched behind the kernel that wrote them,
+// whose end it awaits on the device (programmatic dependent launch).
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnParams p) {
+  constexpr int NW = kJoinThreads / 32, V = D / 32;  // elements per lane
+  __shared__ float2 s_ml[NW];
+  __shared__ float s_o[NW][D];
   const int b = blockIdx.y;
   const SeqView s = seq_view(p.batch, b);
-  const int w = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int tok = w / p.Hq, h = w - tok * p.Hq;
+  const int tok = blockIdx.x / p.Hq, h = blockIdx.x - tok * p.Hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int pieces = 1;
   if (tok < s.nq) {
     const int row = tok * p.group + h % p.group;
@@ -634,40 +689,67 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
   if (pieces == 1) return;
   const size_t at = static_cast<size_t>(s.q0 + tok) * p.Hq + h;
   const float2* ml = p.part_ml + at * p.nsplit;
-  float M = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) M = fmaxf(M, __ldcg(ml + i).x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  constexpr int V = D / 32;  // elements per lane
-  float L = 0.f, a[V];
+  const float* src = p.part_o + at * p.nsplit * D + lane * V;
+  float M = -INFINITY, L = 0.f, a[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) a[e] = 0.f;
-  if (M != -INFINITY) {
-    const float* src = p.part_o + at * p.nsplit * D + lane * V;
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-      const float2 u = __ldcg(ml + i);
-      const float f = ex2(u.x - M);
-      L += u.y * f;
-      float v[V];
+  constexpr int U = 4;  // pieces in flight per warp
+  for (int i0 = warp; i0 < pieces; i0 += NW * U) {
+    float2 u[U];
+    float v[U][V];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * NW < pieces ? i0 + k * NW : i0;
+      u[k] = __ldcg(ml + i);
+      if (i0 + k * NW >= pieces) u[k].x = -INFINITY;
       if constexpr (V == 4) {
         const float4 q = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(i) * D));
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        v[k][0] = q.x; v[k][1] = q.y; v[k][2] = q.z; v[k][3] = q.w;
       } else {
         const float2 q = __ldcg(reinterpret_cast<const float2*>(src + static_cast<size_t>(i) * D));
-        v[0] = q.x; v[1] = q.y;
+        v[k][0] = q.x; v[k][1] = q.y;
       }
+    }
+    float nm = M;
 #pragma unroll
-      for (int e = 0; e < V; ++e) a[e] += v[e] * f;
+    for (int k = 0; k < U; ++k) nm = fmaxf(nm, u[k].x);
+    if (nm == -INFINITY) continue;
+    const float f = ex2(M - nm);
+    M = nm;
+    L *= f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) a[e] *= f;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const float g = ex2(u[k].x - nm);
+      L += u[k].y * g;
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[e] += v[k][e] * g;
     }
   }
-  const float inv = M == -INFINITY ? 0.f : 1.f / L;
-  __nv_bfloat16* dst = p.out + at * D + lane * V;
-  if constexpr (V == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(a[0] * inv, a[1] * inv);
-  if (p.lse != nullptr && lane == 0) p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = a[e];
+  if (lane == 0) s_ml[warp] = make_float2(M, L);
+  __syncthreads();
+  const int d4 = threadIdx.x;
+  if (d4 >= D / 4) return;
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w].x);
+  L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M != -INFINITY)
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float f = ex2(s_ml[w].x - M);
+      const float4 q = *reinterpret_cast<const float4*>(&s_o[w][d4 * 4]);
+      L += s_ml[w].y * f;
+      o.x += q.x * f;
+      o.y += q.y * f;
+      o.z += q.z * f;
+      o.w += q.w * f;
+    }
+  store_row(p, at, d4, D, o, M, L);
 }
 
 }  // namespace ll

@@ -173,6 +173,7 @@ def test_append_refusals(L):
 
 def test_attention_refusals(L):
     sc = swa.ScoreDescC
+    long = _batch(max_kv=200000, max_pages=20000)  # its pieces are joined through the workspace
     bad = (ctypes.c_float * 32)(*([0.0] * 31 + [float("inf")]))
     slopes = sc()
     slopes.slopes = ctypes.cast(bad, ctypes.POINTER(ctypes.c_float))
@@ -183,8 +184,8 @@ def test_attention_refusals(L):
                     (dict(scores=sc(float("inf"))), "softmax_scale"), (dict(scores=sc(0.0, -2.0)), "soft_cap"),
                     (dict(scores=sc(0.0, float("nan"))), "soft_cap"), (dict(scores=sc(0.0, 0.0, -1)), "window"),
                     (dict(scores=sc(0.0, 0.0, 0, -1)), "n_sink"), (dict(scores=sc(0.0, 0.0, 0, 0, A + 2)), "prefix_len"),
-                    (dict(scores=slopes), "slopes[31]"), (dict(ws_bytes=16), "workspace"), (dict(ws=None), "workspace"),
-                    (dict(ws=A + 4), "workspace")]:
+                    (dict(scores=slopes), "slopes[31]"), (dict(batch=long, ws_bytes=16), "workspace"),
+                    (dict(batch=long, ws=None), "workspace"), (dict(batch=long, ws=A + 4), "workspace")]:
         refused(L, _attend(L, **kw), msg)
     refused(L, _attend(L, Hq=136, stride=136 * 128), "exceeds", swa.LL_ERR_UNSUPPORTED)
 
