@@ -163,14 +163,15 @@ AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq
       else if (chunk < 24) chunk = 24;
     }
   } else {
-    // one block per SM: the number of pieces with the least waves x tiles, with 4
-    // tiles' time for a block's start and end and the join's traffic in tiles (a
-    // piece of 256 rows writes and reads 256 KB, about a seventh of a tile per SM)
+    // one block per SM: the number of pieces with the least waves x tiles. A block's start
+    // and end count as 3 tiles, the join as 2 and its traffic (every piece's O in fp32,
+    // written and read) at 16 MB in the time of a tile (2.5 us).
+    const long long piece_bytes = static_cast<long long>(t->total_q) * Hq * c->D * 8;
     long long best = -1;
     for (long long n = 1; n <= 16 && n <= nt; ++n) {
       const long long per = (nt + n - 1) / n;
       const long long waves = (units * n + num_sms() - 1) / num_sms();
-      const long long cost = 100 * waves * (per + 4) + (n > 1 ? 200 + 20 * waves : 0);
+      const long long cost = 100 * waves * (per + 3) + (n > 1 ? 200 + n * piece_bytes / 160000 : 0);
       if (best < 0 || cost < best) {
         best = cost;
         chunk = per;

@@ -9,11 +9,13 @@
 //    (exact). Plain loads rather than TMA boxes because a key tile is 1 to 8
 //    pages, rows that nobody sees are left out (read as zeros) row by row, and the
 //    8-bit tile has to pass through registers anyhow.
-//  * warp 4 issues the MMAs, in halves of 64 keys: S_w = Q_w K^T (both operands in
-//    shared memory) and O_w += P_w V (P in tensor memory, over S_w's columns). While
-//    a softmax warpgroup works on one half of S, the other half is computed: the
-//    softmax, which bounds the kernel, does not wait for its own MMAs. (Whole tiles
-//    of 128 keys, with S and P V in the softmax's way, took 1.8 times as long.)
+//  * warp 4 issues the MMAs: S_w = Q_w K_i^T (both operands in shared memory) and
+//    O_w += P_w V_i (P in tensor memory, over S_w's columns), for the row tiles
+//    w = A, B in turn: one tile's softmax runs under the other's MMAs, which also keeps
+//    the two from wanting the exponential unit at the same time. P is handed over in
+//    halves, so P V begins under the second half's exponentials. (S in halves of 64
+//    keys, double-buffered, so that no softmax ever waited for its own MMAs, ran both
+//    softmaxes in lockstep: 4500 clocks a tile pair.)
 //  * warps 8-11 and 12-15 are A's and B's softmax, a row per thread: maxima and
 //    sums in fp32; O is rescaled in tensor memory only when the reference is
 //    exceeded by 2^8.
@@ -36,22 +38,24 @@ struct PrefillTraits {
   static constexpr int NB = D / 64;              // 128-byte column blocks of a row
   static constexpr int TILE = BN * D * 2;        // one K, V or Q operand tile
   static constexpr int CTRL = 2048;
-  static constexpr int STAGES = (232448 - CTRL - 1024 - 2 * TILE) / TILE < 8
-                                    ? (232448 - CTRL - 1024 - 2 * TILE) / TILE : 8;
-  static constexpr int SMEM = CTRL + 1024 + (2 + STAGES) * TILE;
+  // 8-bit pools: a tile's codes of K and V on their way to fp16
+  static constexpr int RAW = E4M3 ? 2 * BN * D : 0;
+  static constexpr int STAGES = (232448 - CTRL - 1024 - RAW - 2 * TILE) / TILE < 8
+                                    ? (232448 - CTRL - 1024 - RAW - 2 * TILE) / TILE : 8;
+  static constexpr int SMEM = CTRL + 1024 + (2 + STAGES) * TILE + RAW;
   // Slots of per-tile page data. Slot i is written again with buffer K_(i+META),
   // which can only be filled once V_i was consumed (2 META - STAGES >= 1), that is
   // after both softmax warpgroups handed over P_i and so have read slot i.
   static constexpr int META = STAGES / 2 + 1;
   static_assert(2 * META - STAGES >= 1, "meta slots");
   static constexpr int THREADS = 512;
-  // registers: launch 128 per thread (512 x 128 = 65536); loaders 112, the MMA
-  // issuer's warpgroup 48, the softmax warpgroups 176: 112 + 48 + 2 x 176 = 4 x 128
-  static constexpr int LAUNCH_REGS = 128, REGS_LOAD = 112, REGS_MMA = 48, REGS_SOFTMAX = 176;
+  // registers: launch 128 per thread (512 x 128 = 65536); loaders 80, the MMA
+  // issuer's warpgroup 48, the softmax warpgroups 192: 80 + 48 + 2 x 192 = 4 x 128
+  static constexpr int LAUNCH_REGS = 128, REGS_LOAD = 80, REGS_MMA = 48, REGS_SOFTMAX = 192;
   static_assert(REGS_LOAD + REGS_MMA + 2 * REGS_SOFTMAX <= 4 * LAUNCH_REGS, "register split exceeds the launch");
   static constexpr int TMEM_COLS = 512, S_COL = 0, O_COL = 2 * BN;
   static constexpr int FMT = E4M3 ? 0 : 1;       // kind::f16 operands: f16 or bf16
-  static_assert(STAGES >= 5, "the issue order needs five buffers");
+  static_assert(STAGES >= (E4M3 ? 4 : 5), "buffers that the issue order needs: K, V of a tile, the next K, and those in flight");
 };
 
 // What the softmax has to know of 16 keys that lie in one page.
@@ -102,23 +106,21 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                 // [2][TILE]
   uint8_t* sKV = smem + 2 * TILE;     // [STAGES][TILE]
-  uint8_t* ctrl = sKV + STAGES * TILE;
+  uint8_t* sRaw = sKV + STAGES * TILE;  // [2][BN / RPS][128] chunks
+  uint8_t* ctrl = sRaw + TR::RAW;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);  // [STAGES]
   uint64_t* empty = full + 8;                          // [STAGES]
   uint64_t* meta_full = empty + 8;                     // [META]
   uint64_t* q_full = meta_full + TR::META;
-  uint64_t* s_full = q_full + 1;   // [2][2] row tile, half
-  uint64_t* p_ready = s_full + 4;  // [2][2]
-  // A barrier per half: when a softmax thread waits for P V j, the one before on the
-  // same barrier (j - 2) is known to be complete (S j was issued behind it), so a
-  // parity cannot be mistaken for an older phase's.
-  uint64_t* o_done = p_ready + 4;  // [2][2]
-  uint64_t* drain = o_done + 4;
+  uint64_t* s_full = q_full + 1;   // [2] row tile
+  uint64_t* p_ready = s_full + 2;  // [2][2] row tile, half of the keys
+  uint64_t* o_done = p_ready + 4;  // [2]
+  uint64_t* drain = o_done + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* meta_mapped = const_cast<int*>(s_abort) + 1;           // [META]: bit g: keys [16 g, 16 g + 16) have a page
   KeyGroup* meta = reinterpret_cast<KeyGroup*>(ctrl + 512);  // [META][8]
-  static_assert((8 + 8 + TR::META + 14) * 8 + 8 + TR::META * 4 <= 512 && 512 + TR::META * 8 * sizeof(KeyGroup) <= TR::CTRL, "control block");
+  static_assert((8 + 8 + TR::META + 10) * 8 + 8 + TR::META * 4 <= 512 && 512 + TR::META * 8 * sizeof(KeyGroup) <= TR::CTRL, "control block");
 
   asm volatile("griddepcontrol.launch_dependents;");
   // the last rows of a sequence see the most keys: they start first
@@ -145,9 +147,10 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
     }
     for (int i = 0; i < TR::META; ++i) mbar_init(&meta_full[i], 1);
     mbar_init(q_full, two ? 256 : 128);
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_ready[w], 128);
+      mbar_init(&p_ready[2 * w], 128);
+      mbar_init(&p_ready[2 * w + 1], 128);
       mbar_init(&o_done[w], 1);
     }
     mbar_init(drain, 1);
@@ -271,29 +274,31 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       const uint32_t off0 = (c >> 2) * (BN * 128) + sw128_offset(r, (2 * c) & 7);
       const uint32_t off1 = (c >> 2) * (BN * 128) + sw128_offset(r, (2 * c + 1) & 7);
       const size_t lane_off = static_cast<size_t>(r & 15) * D + c * 16;
-      // One tile ahead: each buffer's codes are loaded while the tile before is
-      // converted (2 x 16 KB in flight per SM; one buffer ahead, 6700 clocks a tile
-      // went by waiting for loads).
-      uint4 buf[2][STEPS];
-      auto load_step = [&](const void* pool, int run, int key0, bool whole, int k) -> uint4 {
-        const int at = __shfl_sync(0xffffffffu, run, (r + k * RPS) >> 4);
-        bool valid = at >= 0;
-        if (!whole) valid = valid && kr.some_row_sees(key0 + r + k * RPS);
-        const uint8_t* from = static_cast<const uint8_t*>(pool) + static_cast<size_t>(at) * (16 * D) + lane_off;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (valid)
-          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                       : "l"(from));
-        return u;
+      // The codes come one tile ahead, by asynchronous copies into a place of this
+      // thread's own, which only it reads back. (Ahead in registers they were no faster
+      // than loads waited for at once, 5200 clocks a tile: a warp has six counters for
+      // its outstanding loads, so the wait for one is a wait for the latest.)
+      const uint32_t raw0 = smem_addr(sRaw) + tid * 16;
+      auto fetch = [&](int kv, int i, int run) {  // tile i's codes of K or V
+        if (i < n) {
+          const int key0 = kr.tile(t_beg + i) * BN;
+          const bool whole = whole_tile(key0);
+          const uint8_t* src = static_cast<const uint8_t*>(kv ? p.pool.v : p.pool.k) + lane_off;
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k) {
+            const int row = r + k * RPS;
+            const int at = __shfl_sync(0xffffffffu, run, row >> 4);
+            bool valid = at >= 0;
+            if (!whole) valid = valid && kr.some_row_sees(key0 + row);
+            cp_async16(raw0 + (kv * STEPS + k) * 2048, src + static_cast<size_t>(at < 0 ? 0 : at) * (16 * D), valid);
+          }
+        }
+        cp_async_commit();
       };
-      if (n > 0) {
-        const int key0 = kr.tile(t_beg) * BN, run = run_of(0, pg);
-        const bool whole = whole_tile(key0);
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) buf[0][k] = load_step(p.pool.k, run, key0, whole, k);
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) buf[1][k] = load_step(p.pool.v, run, key0, whole, k);
+      {
+        const int run = run_of(0, pg);
+        fetch(0, 0, run);
+        fetch(1, 0, run);
       }
       for (int i = 0; i < n && ok; ++i) {
         const int pg2 = page_for(i + 2);
@@ -301,17 +306,21 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         // V's scale without its exponent, for the 16 keys of lane g
         const float mant = vs * exp2f(-scale_exponent(vs));
         const bool plain = __all_sync(0xffffffffu, lane >= 8 || mant == 1.f);
-        const bool more = i + 1 < n;
-        const int key1 = more ? kr.tile(t_beg + i + 1) * BN : 0, run1 = run_of(i + 1, pg1);
-        const bool whole1 = whole_tile(key1);
-#pragma unroll
+        const int run1 = run_of(i + 1, pg1);
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
+          cp_async_wait<1>();  // this buffer's copies; the other's may be in flight
+          uint4 buf[STEPS];
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k)
+            buf[k] = *reinterpret_cast<const uint4*>(sRaw + (kv * STEPS + k) * 2048 + tid * 16);
+          fetch(kv, i + 1, run1);
           wait_empty(st, round);
           if (!ok) break;
           uint8_t* dst = sKV + st * TILE;
 #pragma unroll
           for (int k = 0; k < STEPS; ++k) {
-            const uint32_t w[4] = {buf[kv][k].x, buf[kv][k].y, buf[kv][k].z, buf[kv][k].w};
+            const uint32_t w[4] = {buf[k].x, buf[k].y, buf[k].z, buf[k].w};
             uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) e4m3x4_f16(w[e], h[2 * e], h[2 * e + 1]);
@@ -325,7 +334,6 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
             }
             *reinterpret_cast<uint4*>(dst + off0 + k * (RPS * 128)) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4*>(dst + off1 + k * (RPS * 128)) = make_uint4(h[4], h[5], h[6], h[7]);
-            if (more) buf[kv][k] = load_step(kv ? p.pool.v : p.pool.k, run1, key1, whole1, k);
           }
           if (kv == 0) put_meta(i);
           publish(st);
@@ -336,6 +344,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         ks = ks1;
         vs = vs1;
       }
+      cp_async_wait<0>();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ MMA issuer
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       // The whole warp walks the loop, so that its control flow and the descriptors
       // are uniform (a branch on the lane makes every operand of every MMA a move
       // into a uniform register first); one elected lane issues.
-      constexpr uint32_t idS = idesc_dense(BM, TR::HN, TR::FMT, false, false);
+      constexpr uint32_t idS = idesc_dense(BM, BN, TR::FMT, false, false);
       constexpr uint32_t idO = idesc_dense(BM, D, TR::FMT, false, true);
       const uint32_t hi = desc_words(0, 0, 1024, 2).hi;
       const uint32_t q_lo = desc_words(smem_addr(sQ), 16, 1024, 2).lo;
@@ -357,35 +366,33 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       auto commit = [&](uint64_t* bar) {
         if (leader) mma_commit(bar);
       };
-      auto issue_s = [&](int w, int h, int st) {
-        const DescWords q{q_lo + w * (TILE >> 4), hi};
-        const DescWords kd{k_lo + st * (TILE >> 4) + h * (TR::HN * 128 >> 4), hi};
-        const uint32_t d = tbase + TR::S_COL + w * BN + h * TR::HN;
+      auto issue_s = [&](int w, int st) {
+        const DescWords q{q_lo + w * (TILE >> 4), hi}, kd{k_lo + st * (TILE >> 4), hi};
+        const uint32_t d = tbase + TR::S_COL + w * BN;
         if (leader) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = (k >> 2) * (BM * 128) + (k & 3) * 32;
             mma_bf16_ss(d, desc_at(q, off), desc_at(kd, off), idS, k > 0);
           }
-          mma_commit(&s_full[2 * w + h]);
+          mma_commit(&s_full[w]);
         }
       };
-      auto issue_pv = [&](int w, int h, int st, bool first) {
+      auto issue_pv = [&](int w, int h, int st, bool first, bool last) {
         const DescWords v{v_lo + st * (TILE >> 4) + h * (TR::HN * 128 >> 4), hi};
-        const uint32_t d = tbase + TR::O_COL + w * D, a = tbase + TR::S_COL + w * BN + h * TR::HN;
+        const uint32_t d = tbase + TR::O_COL + w * D, a = tbase + TR::S_COL + w * BN + h * (TR::HN / 2);
         if (leader) {
 #pragma unroll
           for (int k = 0; k < TR::HN / 16; ++k)
             mma_bf16_ts(d, a + k * 8, desc_at(v, k * 16 * 128), idO, !first || k > 0);
-          mma_commit(&o_done[2 * w + h]);
+          if (last) mma_commit(&o_done[w]);
         }
       };
       const int tiles = two ? 2 : 1;
       bool ok = wait(q_full, 0) && wait(&full[0], 0);
       if (ok) {
         tc_fence_after();
-        for (int h = 0; h < 2; ++h)
-          for (int w = 0; w < tiles; ++w) issue_s(w, h, 0);
+        for (int w = 0; w < tiles; ++w) issue_s(w, 0);
         commit(&empty[0]);
       }
       int st = 1, round = 0;  // buffer of V_i and its use
@@ -394,18 +401,20 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         if (!(ok = wait(&full[st], round & 1))) break;
         const int v_st = st;
         if (++st == STAGES) st = 0, ++round;
-        for (int h = 0; ok && h < 2; ++h)
-          for (int w = 0; w < tiles; ++w) {
+        for (int w = 0; w < tiles; ++w) {
+          for (int h = 0; ok && h < 2; ++h) {
             if (!(ok = wait(&p_ready[2 * w + h], i & 1))) break;
             tc_fence_after();
-            issue_pv(w, h, v_st, i == 0 && h == 0);
-            if (!more) continue;
-            if (h == 0 && w == 0) {
-              if (!(ok = wait(&full[st], round & 1))) break;
-              tc_fence_after();
-            }
-            issue_s(w, h, st);
+            issue_pv(w, h, v_st, i == 0 && h == 0, !more && h == 1);
           }
+          if (!ok) break;
+          if (!more) continue;
+          if (w == 0) {
+            if (!(ok = wait(&full[st], round & 1))) break;
+            tc_fence_after();
+          }
+          issue_s(w, st);
+        }
         if (!ok) break;
         commit(&empty[v_st]);
         if (more) {
@@ -495,28 +504,26 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       const float slope = MODS & kBiased ? p.sc.slope2[h] : 0.f;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < 2 * n; ++j) {  // halves of key tiles
-        const int i = j >> 1, h2 = j & 1;
-        if (h2 == 0) ok = __all_sync(0xffffffffu, mbar_wait(&meta_full[i % TR::META], (i / TR::META) & 1, s_abort));
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * w + h2], i & 1, s_abort));
+      for (int i = 0; i < n; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&meta_full[i % TR::META], (i / TR::META) & 1, s_abort));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], i & 1, s_abort));
         if (!ok) break;
         tc_fence_after();
-        const KeyGroup* kg = meta + (i % TR::META) * 8 + h2 * 4;
-        const unsigned mapped = (static_cast<unsigned>(meta_mapped[i % TR::META]) >> (4 * h2)) & 15u;
-        const int key0 = kr.tile(t_beg + i) * BN + h2 * TR::HN;
-        const uint32_t tH = tS + h2 * TR::HN;
-        uint32_t sr[2][32];
-        tmem_load32(tH, sr[0]);
-        tmem_load32(tH + 32, sr[1]);
-        tmem_load_wait(sr[0]);
-        tmem_load_wait(sr[1]);
-        const bool all_seen = mapped == 15u && (key0 + TR::HN <= kr.prefix ||
-                                                (key0 + TR::HN - 1 <= w_lo && key0 + TR::HN <= s.len &&
-                                                 (p.sc.window == 0 || w_hi - key0 < p.sc.window)));
-        if constexpr (MODS != 0) {
-          const float away = MODS & kBiased ? offset_of(pos, key0) : 0.f;  // of key 0 of the half
+        const KeyGroup* kg = meta + (i % TR::META) * 8;
+        const unsigned mapped = static_cast<unsigned>(meta_mapped[i % TR::META]);
+        const int key0 = kr.tile(t_beg + i) * BN;
+        uint32_t sr[4][32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 4; ++c) tmem_load32(tS + c * 32, sr[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load_wait(sr[c]);
+        const bool all_seen = mapped == 255u && (key0 + BN <= kr.prefix ||
+                                                 (key0 + BN - 1 <= w_lo && key0 + BN <= s.len &&
+                                                  (p.sc.window == 0 || w_hi - key0 < p.sc.window)));
+        if constexpr (MODS != 0) {
+          const float away = MODS & kBiased ? offset_of(pos, key0) : 0.f;  // of key 0 of the tile
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               sr[c][e] = __float_as_uint(score2<MODS>(p.sc, __uint_as_float(sr[c][e]),
@@ -526,7 +533,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         if (!all_seen) {
           const int a = sees_a - key0, bb = sees_b - key0, ee = sees_e - key0;
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const int k = c * 32 + e;
@@ -536,26 +543,24 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         }
         // factor on the scores of group g (kept off 0, so that masked ones stay -inf)
         auto factor = [&](int g) { return MODS != 0 ? 1.f : (E4M3 ? fmaxf(fac * kg[g].ks, 1e-37f) : fac); };
-        float mx = -INFINITY;
+        float mg[8];  // maxima of the groups, chains of their own
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 8; ++g) {
           const uint32_t* v = &sr[g >> 1][(g & 1) * 16];
           float q[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             q[e] = fmax3(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
                          fmaxf(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])));
-          const float x = fmaxf(fmax3(q[0], q[1], q[2]), q[3]);
-          mx = E4M3 ? fmaxf(mx, fmaf(x, factor(g), kg[g].c)) : fmaxf(mx, x);
+          mg[g] = fmaxf(fmax3(q[0], q[1], q[2]), q[3]);
+          if (E4M3) mg[g] = fmaf(mg[g], factor(g), kg[g].c);
         }
+        float mx = fmaxf(fmax3(fmax3(mg[0], mg[1], mg[2]), mg[3], mg[4]), fmax3(mg[5], mg[6], mg[7]));
         if (!E4M3) mx *= factor(0);
         const bool raise = mx > m + 8.f;
         const float m_use = raise ? mx : m;
-        if (__any_sync(0xffffffffu, raise) && j > 0) {
-          // O is this warpgroup's alone once the last P V is complete
-          ok = __all_sync(0xffffffffu, mbar_wait(&o_done[2 * w + (h2 ^ 1)], ((j - 1) >> 1) & 1, s_abort));
-          if (!ok) break;
-          tc_fence_after();
+        // S_i complete implies that P V i - 1, issued before it, is
+        if (__any_sync(0xffffffffu, raise) && i > 0) {
           const float al = raise ? ex2(m - m_use) : 1.f;
           l *= al;
 #pragma unroll 1
@@ -572,7 +577,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         const float ms = m == -INFINITY ? 0.f : m;
         uint64_t l2 = 0ull;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 4; ++c) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int g = 2 * c + hf;
@@ -594,17 +599,19 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
             if constexpr (E4M3) l2 = f2_fma(sum, f2_pack(kg[g].inv_c, kg[g].inv_c), l2);
             else l2 = f2_add(l2, sum);
           }
-          tmem_store16(tH + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&sr[c][0]));
+          tmem_store16(tS + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&sr[c][0]));
+          if (c & 1) {  // 64 keys of P are on their way
+            tmem_store_wait();
+            tc_fence_before();
+            mbar_arrive(&p_ready[2 * w + (c >> 1)]);
+          }
         }
         float u0, u1;
         f2_unpack(l2, u0, u1);
         l += u0 + u1;
-        tmem_store_wait();
-        tc_fence_before();
-        mbar_arrive(&p_ready[2 * w + h2]);
       }
       // ---- epilogue
-      if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[2 * w + 1], (n - 1) & 1, s_abort));
+      if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[w], 0, s_abort));
       tc_fence_after();
       if (ok) {
         const size_t at = static_cast<size_t>(s.q0 + tok) * p.Hq + h;
