@@ -599,12 +599,17 @@ def _device(t: torch.Tensor) -> int:
     return torch.cuda.current_device() if t.is_cuda else -2
 
 
-def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    """A new tensor that belongs to the stream the kernels run on."""
+def _empty_rows(like: torch.Tensor, stream) -> torch.Tensor:
+    """A contiguous tensor of `like`'s shape that belongs to the stream the kernels run on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+
+def _workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    with torch.cuda.stream(stream):  # None: the current stream
+        return like.new_empty((nbytes,), dtype=torch.uint8)
 
 
 def token_rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: TokenRope, transpose: bool = False,
@@ -614,9 +619,10 @@ def token_rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: TokenRope, 
     dev = _device(x)
     xp, xs = _rows(x, "x", dev)
     T, H, D = x.shape
-    _expect(positions, (T,), torch.int32, "positions")
+    if positions.dtype != torch.int32 or positions.shape != (T,):
+        _expect(positions, (T,), torch.int32, "positions")
     if out is None:
-        out = _empty(x.shape, x.dtype, x, stream)
+        out = _empty_rows(x, stream)
         op, os_ = out.data_ptr(), H * D
     else:
         if out.dtype != x.dtype or out.shape != x.shape:
@@ -663,7 +669,7 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: TokenBatch, rop
     qp, qs = _rows(q, "q", dev, None, cache.D)
     T, Hq, D = q.shape
     if out is None:
-        out = _empty((T, Hq, D), q.dtype, q, stream)
+        out = _empty_rows(q, stream)
         op = out.data_ptr()
     else:
         _expect(out, (T, Hq, D), q.dtype, "out")
@@ -675,11 +681,11 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: TokenBatch, rop
     if T == 0:
         return out
     L, pool, tokens = lib(), cache.to_c(dev), batch.to_c(T, dev)
-    wp, ws_bytes = None, 0
+    wp = None
     if workspace is None:
         ws_bytes = L.ll_paged_attention_workspace_bytes(pool, tokens, Hq)
         if ws_bytes:
-            workspace = _empty((ws_bytes,), torch.uint8, q, stream)
+            workspace = _workspace(ws_bytes, q, stream)
             wp = workspace.data_ptr()
     else:
         wp, ws_bytes = _on(workspace, dev), workspace.numel() * workspace.element_size()

@@ -51,7 +51,7 @@ struct KeyRange {
   int prefix, always, lo, upper;  // keys [0, always) and [lo, upper) are seen by some row
   int a_end, w_beg, nt;           // tiles in all
   __device__ __forceinline__ int tile(int i) const { return i < a_end ? i : i - a_end + w_beg; }
-  __device__ __forceinline__ bool some_row_sees(int j) const { return j < always || (j >= lo && j < upper); }
+  __device__ __forceinline__ bool some_row_sees(int j) const { return (j < always) | ((j >= lo) & (j < upper)); }
 };
 
 // The first key that the window of position p reaches.
@@ -77,8 +77,9 @@ __device__ __forceinline__ KeyRange key_range(const ScoreParams& sc, int b, cons
 }
 
 __device__ __forceinline__ bool row_sees(const ScoreParams& sc, const KeyRange& r, int len, int p, int j) {
-  if (j < r.prefix) return true;
-  return j <= p && j < len && (sc.window == 0 || p - j < sc.window || j < sc.n_sink);
+  // bitwise: short-circuits would be branches
+  const bool near = static_cast<unsigned>(p) - static_cast<unsigned>(j) < static_cast<unsigned>(sc.window);
+  return (j < r.prefix) | ((j <= p) & (j < len) & ((sc.window == 0) | near | (j < sc.n_sink)));
 }
 
 // Positions of a unit's first and last row.

@@ -440,37 +440,36 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       {
         const __nv_bfloat16* src = p.q + static_cast<long long>(s.q0 + (live ? tok : 0)) * p.q_stride + h * D;
         uint8_t* dst = sQ + w * TILE;
+        uint4 raw[D / 8];  // the whole row in flight at once
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          int lo, hi;
+          item_chunks(p.rope, c, lo, hi);
+          raw[2 * c] = live ? *reinterpret_cast<const uint4*>(src + lo * 8) : make_uint4(0u, 0u, 0u, 0u);
+          raw[2 * c + 1] = live ? *reinterpret_cast<const uint4*>(src + hi * 8) : make_uint4(0u, 0u, 0u, 0u);
+        }
         float inv = 1.f;
         if constexpr (E4M3) {  // fp16 under a power of two (see the decode kernel); a rotated element is below 2 amp max
-          float a = 0.f;
-          if (live)
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              float x[8];
-              load_chunk8<__nv_bfloat16>(src + c * 8, x);
+          __nv_bfloat162 a2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
-            }
+          for (int c = 0; c < D / 8; ++c) a2 = bf16_amax(raw[c], a2);
+          float a = fmaxf(__low2float(a2), __high2float(a2));
           if (p.rope.rot > 0) a *= fmaxf(fabsf(p.rope.amp), 1.f);
           qf = power_below(a);
           inv = 1.f / qf;
         }
-#pragma unroll 2
+#pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           int lo, hi;
           item_chunks(p.rope, c, lo, hi);
           float x[8], y[8];
+          unpack8(raw[2 * c], x);
+          unpack8(raw[2 * c + 1], y);
+          if (c < (p.rope.rot >> 4)) {
+            float2 cs[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-          if (live) {
-            load_chunk8<__nv_bfloat16>(src + lo * 8, x);
-            load_chunk8<__nv_bfloat16>(src + hi * 8, y);
-            if (c < (p.rope.rot >> 4)) {
-              float2 cs[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) cs[e] = turn_fast(p.rope, pos, c * 8 + e);
-              rotate_item(p.rope, x, y, cs, 1);
-            }
+            for (int e = 0; e < 8; ++e) cs[e] = turn_fast(p.rope, pos, c * 8 + e);
+            rotate_item(p.rope, x, y, cs, 1);
           }
           uint32_t u[8];
 #pragma unroll
@@ -531,15 +530,17 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
                                                       away - static_cast<float>(c * 32 + e)));
         }
         if (!all_seen) {
-          const int a = sees_a - key0, bb = sees_b - key0, ee = sees_e - key0;
+          // 32 keys' visibility as bits, a test and a select per score (conditions joined
+          // by && and || became branches: a masked tile took four times an open one)
+          auto below = [](int x) { return x <= 0 ? 0u : (x >= 32 ? ~0u : (1u << x) - 1u); };
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const int k0 = key0 + c * 32;
+            unsigned seen = below(sees_a - k0) | (below(sees_e - k0) & ~below(sees_b - k0));
+            seen &= (mapped >> (2 * c) & 1u ? 0xFFFFu : 0u) | (mapped >> (2 * c + 1) & 1u ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int k = c * 32 + e;
-              const bool seen = (k < a || (k >= bb && k < ee)) && (mapped >> (2 * c + (e >> 4)) & 1u);
-              if (!seen) sr[c][e] = __float_as_uint(-INFINITY);
-            }
+            for (int e = 0; e < 32; ++e) sr[c][e] = seen & (1u << e) ? sr[c][e] : __float_as_uint(-INFINITY);
+          }
         }
         // factor on the scores of group g (kept off 0, so that masked ones stay -inf)
         auto factor = [&](int g) { return MODS != 0 ? 1.f : (E4M3 ? fmaxf(fac * kg[g].ks, 1e-37f) : fac); };

@@ -178,22 +178,40 @@ __global__ void __launch_bounds__(kTokenRopeThreads) token_rope_kernel(const Tok
   extern __shared__ float2 s_cs[];
   const int t0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, p.T - t0);
-  const TurnTable tab = make_turn_table(p.rope, s_cs, nt, [&](int t) { return p.positions[t0 + t]; });
   const int per_head = p.D >> 4, per_token = p.H * per_head;
   const int items = nt * per_token;
-  for (int i = threadIdx.x; i < items; i += blockDim.x) {
-    const int t = i / per_token, r = i - t * per_token;
-    const int h = r / per_head, c = r - h * per_head;
-    int lo, hi;
-    item_chunks(p.rope, c, lo, hi);
-    const T* src = static_cast<const T*>(p.x) + (t0 + t) * p.x_stride + h * p.D;
-    T* dst = static_cast<T*>(p.out) + (t0 + t) * p.out_stride + h * p.D;
-    float a[8], b[8];
-    load_chunk8<T>(src + lo * 8, a);
-    load_chunk8<T>(src + hi * 8, b);
-    if (c < (p.rope.rot >> 4)) rotate_item(p.rope, a, b, tab.unit(t, c), tab.step);
-    store_chunk8<T>(dst + lo * 8, a);
-    store_chunk8<T>(dst + hi * 8, b);
+  // a unit's place, and its two chunks
+  struct Unit {
+    int t, c, lo, hi;
+    const T* src;
+    T* dst;
+  };
+  auto unit_of = [&](int i) {
+    Unit u;
+    u.t = i / per_token;
+    const int r = i - u.t * per_token, h = r / per_head;
+    u.c = r - h * per_head;
+    item_chunks(p.rope, u.c, u.lo, u.hi);
+    u.src = static_cast<const T*>(p.x) + (t0 + u.t) * p.x_stride + h * p.D;
+    u.dst = static_cast<T*>(p.out) + (t0 + u.t) * p.out_stride + h * p.D;
+    return u;
+  };
+  float a[8], b[8];
+  auto load = [&](const Unit& u) {
+    load_chunk8<T>(u.src + u.lo * 8, a);
+    load_chunk8<T>(u.src + u.hi * 8, b);
+  };
+  // the first unit's loads are in flight while the table is made
+  int i = threadIdx.x;
+  Unit u{};
+  if (i < items) load(u = unit_of(i));
+  const TurnTable tab = make_turn_table(p.rope, s_cs, nt, [&](int t) { return p.positions[t0 + t]; });
+  while (i < items) {
+    if (u.c < (p.rope.rot >> 4)) rotate_item(p.rope, a, b, tab.unit(u.t, u.c), tab.step);
+    store_chunk8<T>(u.dst + u.lo * 8, a);
+    store_chunk8<T>(u.dst + u.hi * 8, b);
+    i += blockDim.x;
+    if (i < items) load(u = unit_of(i));
   }
 }
 
