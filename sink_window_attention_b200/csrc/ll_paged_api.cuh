@@ -362,11 +362,13 @@ ll_status ll_paged_append(const ll_paged_cache* cache, const ll_token_batch* bat
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int pairs = p.rope.rot / 2, ps = cache->page_size;
   if (cache->dtype == LL_BF16) {
+    // tokens per block: a thread's share of them in flight, while that leaves 4 blocks to an SM
     const int per_token = cache->H * (cache->D / 16);
-    int tokens = 2 * ll::kPagedAppendThreads / per_token;
+    const int abreast = per_token < ll::kPagedAppendThreads ? ll::kPagedAppendThreads / per_token : 1;
     const long long fill = static_cast<long long>(max_q) * batch->B / (4 * num_sms());
-    if (tokens > fill) tokens = static_cast<int>(fill);
-    p.tokens = tokens < 1 ? 1 : (tokens > 16 ? 16 : tokens);
+    int tokens = abreast * ll::kAppendAhead;
+    if (tokens > ll::kAppendMaxTokens) tokens = ll::kAppendMaxTokens;
+    p.tokens = tokens < fill ? tokens : (fill < 1 ? 1 : static_cast<int>(fill));
     ll::paged_append_bf16_kernel<<<dim3((max_q - 1) / p.tokens + 1, batch->B), ll::kPagedAppendThreads,
                                    ll::turn_table_bytes(p.tokens, pairs), s>>>(p);
     return check_launch("paged_append_bf16_kernel");

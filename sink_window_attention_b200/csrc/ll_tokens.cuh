@@ -240,41 +240,79 @@ struct PagedAppendParams {
 constexpr int kPagedAppendThreads = 256;
 constexpr int kPagedAppendMaxThreads = 1024;  // 8-bit pool: a thread per 16 elements of a page and head
 
-// BF16 pool: a block takes `tokens` tokens of one sequence, all heads.
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// BF16 pool: a block takes `tokens` tokens of one sequence, all heads. A thread keeps
+// its head and chunks and goes from token to token, kAppendAhead of them in flight, so
+// nothing is divided or looked up per unit (with a division and a page table read for
+// each, 13 us for 7800 tokens of 12 heads of 128; floor 7.3).
+constexpr int kAppendAhead = 2, kAppendMaxTokens = 32;
+
 __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_bf16_kernel(const PagedAppendParams p) {
   extern __shared__ float2 s_cs[];
+  __shared__ long long s_row[kAppendMaxTokens];  // first row of the token's page, all heads', plus its row; -1: none
   const int b = blockIdx.y;
   const SeqView s = seq_view(p.batch, b);
   const int i0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, s.nq - i0);
   if (nt <= 0) return;
-  const TurnTable tab = make_turn_table(p.rope, s_cs, nt, [&](int t) { return s.first_pos + i0 + t; });
-  const int D = p.pool.D, H = p.pool.H, ps = p.pool.page_size;
-  const int per_head = D >> 4, per_token = H * per_head;
-  for (int i = threadIdx.x; i < nt * per_token; i += blockDim.x) {
-    const int t = i / per_token, r = i - t * per_token;
-    const int h = r / per_head, c = r - h * per_head;
+  const int D = p.pool.D, H = p.pool.H, shift = p.pool.page_shift;
+  for (int t = threadIdx.x; t < nt; t += blockDim.x) {
     const int pos = s.first_pos + i0 + t;
-    if (pos < 0 || pos >> p.pool.page_shift >= p.batch.max_pages) continue;
-    const int page = page_of(p.batch, b, pos >> p.pool.page_shift, p.pool.n_pages);
-    if (page < 0) continue;
+    int page = -1;
+    if (pos >= 0 && pos >> shift < p.batch.max_pages) page = page_of(p.batch, b, pos >> shift, p.pool.n_pages);
+    s_row[t] = page < 0 ? -1 : (static_cast<long long>(page) * H << shift) + (pos & (p.pool.page_size - 1));
+  }
+  const int log_units = D == 128 ? 3 : 2;  // units of 16 elements in a head
+  const int per_token = H << log_units;
+  const int abreast = per_token < kPagedAppendThreads ? kPagedAppendThreads / per_token : 1;  // tokens at a time
+  const int t_mine = threadIdx.x / per_token, u0 = threadIdx.x - t_mine * per_token;
+  const TurnTable tab = make_turn_table(p.rope, s_cs, nt, [&](int t) { return s.first_pos + i0 + t; });
+  if (t_mine >= abreast) return;
+  for (int u = u0; u < per_token; u += kPagedAppendThreads) {
+    const int h = u >> log_units, c = u & ((1 << log_units) - 1);
     int lo, hi;
     item_chunks(p.rope, c, lo, hi);
-    const size_t row = s.q0 + i0 + t;
-    const __nv_bfloat16* kr = p.k + row * p.k_stride + h * D;
-    const __nv_bfloat16* vr = p.v + row * p.v_stride + h * D;
-    const uint4 v0 = *reinterpret_cast<const uint4*>(vr + lo * 8), v1 = *reinterpret_cast<const uint4*>(vr + hi * 8);
-    float x[8], y[8];
-    load_chunk8<__nv_bfloat16>(kr + lo * 8, x);
-    load_chunk8<__nv_bfloat16>(kr + hi * 8, y);
-    if (c < (p.rope.rot >> 4)) rotate_item(p.rope, x, y, tab.unit(t, c), tab.step);
-    const size_t at = ((static_cast<size_t>(page) * H + h) * ps + (pos & (ps - 1))) * D;
-    __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(p.pool.k) + at;
-    __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.pool.v) + at;
-    store_chunk8<__nv_bfloat16>(kd + lo * 8, x);
-    store_chunk8<__nv_bfloat16>(kd + hi * 8, y);
-    *reinterpret_cast<uint4*>(vd + lo * 8) = v0;
-    *reinterpret_cast<uint4*>(vd + hi * 8) = v1;
+    const bool turns = c < (p.rope.rot >> 4);
+    const __nv_bfloat16* kr = p.k + static_cast<size_t>(s.q0 + i0) * p.k_stride + h * D;
+    const __nv_bfloat16* vr = p.v + static_cast<size_t>(s.q0 + i0) * p.v_stride + h * D;
+    __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(p.pool.k);
+    __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.pool.v);
+    for (int t0 = t_mine; t0 < nt; t0 += abreast * kAppendAhead) {
+      uint4 raw[kAppendAhead][4];
+#pragma unroll
+      for (int k = 0; k < kAppendAhead; ++k) {
+        const int t = t0 + k * abreast;
+        if (t < nt) {
+          raw[k][0] = *reinterpret_cast<const uint4*>(kr + t * p.k_stride + lo * 8);
+          raw[k][1] = *reinterpret_cast<const uint4*>(kr + t * p.k_stride + hi * 8);
+          raw[k][2] = *reinterpret_cast<const uint4*>(vr + t * p.v_stride + lo * 8);
+          raw[k][3] = *reinterpret_cast<const uint4*>(vr + t * p.v_stride + hi * 8);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAppendAhead; ++k) {
+        const int t = t0 + k * abreast;
+        if (t >= nt || s_row[t] < 0) continue;
+        const size_t at = static_cast<size_t>(s_row[t] + (static_cast<long long>(h) << shift)) * D;
+        float x[8], y[8];
+        unpack8(raw[k][0], x);
+        unpack8(raw[k][1], y);
+        if (turns) rotate_item(p.rope, x, y, tab.unit(t, c), tab.step);
+        store_chunk8<__nv_bfloat16>(kd + at + lo * 8, x);
+        store_chunk8<__nv_bfloat16>(kd + at + hi * 8, y);
+        *reinterpret_cast<uint4*>(vd + at + lo * 8) = raw[k][2];
+        *reinterpret_cast<uint4*>(vd + at + hi * 8) = raw[k][3];
+      }
+    }
   }
 }
 
@@ -321,16 +359,6 @@ __device__ __forceinline__ uint2 recode8(uint2 c, float ratio) {
     x[2 * i + 1] = f.y;
   }
   return encode8(x, ratio);
-}
-
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
 }
 
 // The largest |x| of eight bf16 values, NaN left out.
