@@ -433,7 +433,8 @@ ll_status ll_token_rope_apply(const void* x, long long x_stride, void* out, long
  * one page and head lie together.
  * k_scale, v_scale: [n_pages][H] fp32, FP8 only (NULL otherwise): one scale for
  * each block of page_size tokens and head; value = decode(code) * scale.
- * page_size: 16, 32, 64 or 128; D: 64 or 128; 16-byte aligned k and v.
+ * page_size: 16, 32, 64 or 128; D: 64 or 128; H at most LL_MAX_TOKEN_HEADS;
+ * n_pages * H * page_size / 16 at most 2^31 - 1; k and v 16-byte aligned, the scales 4.
  */
 typedef struct ll_paged_cache {
   void* k;
@@ -455,8 +456,8 @@ typedef struct ll_paged_cache {
  * are DEVICE int32 arrays, read when the call runs; max_q and max_kv are the
  * host's bounds on the rows and the length of a sequence.
  * What the arrays say is bounded on the device: rows from max_q on and rows
- * beyond total_q are not processed; keys beyond max_kv or max_pages * page_size
- * do not exist; an entry of page_table outside [0, n_pages) names no page (its
+ * beyond total_q are not processed; keys beyond max_kv, max_pages * page_size or
+ * 2^31 - 257 do not exist; an entry of page_table outside [0, n_pages) names no page (its
  * keys do not exist, tokens appended there are dropped), so pages that no query
  * sees any more may be given back and their entries set to -1. Rows of no
  * sequence are left as they are.
@@ -465,7 +466,7 @@ typedef struct ll_token_batch {
   const int32_t* q_start;
   const int32_t* kv_len;
   const int32_t* page_table;
-  int B, max_pages;
+  int B, max_pages;  /* B at most 65535 */
   int total_q;       /* rows of the token tensors */
   int max_q, max_kv;
 } ll_token_batch;
@@ -478,7 +479,7 @@ typedef struct ll_token_batch {
  * becomes s = max(s_old, the smallest power of two with 448 s >= max|x| over the
  * page's new tokens), s_old being the stored scale where the page holds earlier
  * tokens of the sequence (new tokens do not begin at its row 0) and 0 otherwise;
- * new codes are RNE(x / s) saturated (0 where s is 0), and where s grew over
+ * new codes are RNE(x / s) saturated (where s is 0: 0, NaN for a non-finite x), and where s grew over
  * s_old the earlier tokens' codes become RNE(code * s_old / s). Powers of two
  * make that re-coding exact but for underflow: a page filled token by token
  * carries one rounding, like one that is written at once. max|x| is taken over
@@ -518,7 +519,8 @@ typedef struct ll_score_desc {
  * out = softmax(scores) V for the batch's rows, over the pool that already holds
  * them (append first). q, out: [total_q][Hq][D] BF16; Hq a multiple of the
  * pool's H, query head h reads K/V head h / (Hq / H). q is rotated at its
- * positions when rope != NULL. out rows are contiguous (stride Hq * D).
+ * positions when rope != NULL. out rows are contiguous (stride Hq * D); out and lse
+ * overlap no input.
  * A row that sees no key gets 0, and -inf in lse. lse (optional): [total_q][Hq]
  * fp32, natural-log sum of exp of the final scores.
  * Keys that no query of a tile of rows sees are not read, so what their places
@@ -533,9 +535,9 @@ typedef struct ll_score_desc {
  * Errors: LL_ERR_INVALID_ARG for NULL or misaligned pointers, an invalid cache,
  * batch or rope descriptor, a q_dtype other than BF16, Hq not a multiple of H,
  * a q_stride that is no multiple of 8 or < Hq * D, a negative or non-finite
- * softmax_scale or soft_cap, negative window or n_sink, a slope that is not
- * finite, a workspace that is too small; LL_ERR_UNSUPPORTED for Hq >
- * LL_MAX_TOKEN_HEADS or H * B > 2^20.
+ * softmax_scale or soft_cap (or a quotient of them outside fp32's range), negative
+ * window or n_sink, a slope that is not finite, a workspace that is too small;
+ * LL_ERR_UNSUPPORTED for Hq > LL_MAX_TOKEN_HEADS or more than 2^31 - 1 blocks.
  */
 size_t ll_paged_attention_workspace_bytes(const ll_paged_cache* cache, const ll_token_batch* batch, int Hq);
 

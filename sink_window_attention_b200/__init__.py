@@ -506,17 +506,18 @@ class PagedKVCache:
             self.k_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
             self.v_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
         self.code = LL_FP8_E4M3 if dtype == "fp8" else LL_BF16
-        self._at, self._c = None, None
+        self._kept = ((), None)  # addresses and descriptor, replaced together
 
     def to_c(self, device: Optional[int] = None) -> PagedCacheC:
         """The descriptor; with a device, its tensors are checked to be there."""
         tensors = (self.k, self.v) if self.k_scale is None else (self.k, self.v, self.k_scale, self.v_scale)
         at = tuple([t.data_ptr() if device is None else _on(t, device) for t in tensors])
-        if at != self._at:
-            self._c = PagedCacheC(*(at if len(at) == 4 else at + (None, None)), self.code, self.n_pages, self.page_size,
-                                  self.H, self.D)
-            self._at = at
-        return self._c
+        kept, c = self._kept
+        if at != kept:
+            c = PagedCacheC(*(at if len(at) == 4 else at + (None, None)), self.code, self.n_pages, self.page_size,
+                            self.H, self.D)
+            self._kept = (at, c)
+        return c
 
 
 class TokenBatch:
@@ -537,17 +538,16 @@ class TokenBatch:
         _expect(kv_len, (B,), torch.int32, "kv_len")
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
         self.B, self.max_pages, self.max_q, self.max_kv = B, max_pages, int(max_q), int(max_kv)
-        self._key, self._c = None, None
+        self._kept = ((), None)  # fields and descriptor, replaced together
 
     def to_c(self, total_q: int, device: int) -> TokenBatchC:
         key = (_on(self.q_start, device), _on(self.kv_len, device), _on(self.page_table, device), self.B,
                self.max_pages, total_q, self.max_q, self.max_kv)
-        if key != self._key:
-            # a new structure, not a changed one: another thread may be in a call with the old
+        kept, c = self._kept
+        if key != kept:  # a new structure, not a changed one: another thread may be in a call with the old
             c = TokenBatchC(*key)
-            self._key, self._c = key, c
-            return c
-        return self._c
+            self._kept = (key, c)
+        return c
 
 
 class Scores:

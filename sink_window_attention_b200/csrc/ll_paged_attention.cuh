@@ -636,6 +636,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   if (p.clustered && pieces > 1) {
     // the cluster's blocks join their rows through each other's shared memory, a share
     // of the elements each
+    __syncwarp();
     cluster_barrier();
     for (int i = threadIdx.x + split * TR::THREADS; i < ROWS * (D / 4); i += pieces * TR::THREADS) {
       const int r = i / (D / 4), d4 = i % (D / 4);
@@ -658,6 +659,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
       const size_t at = static_cast<size_t>(s.q0 + row / p.group) * p.Hq + hkv * p.group + row % p.group;
       store_row(p, at, d4, D, a, M, L);
     }
+    __syncwarp();
     cluster_barrier();  // nobody leaves while its shared memory is read
   }
 }

@@ -442,6 +442,62 @@ def test_scales_far_apart_and_large_scores(dtype, D, new):
     assert torch.all(out == 0)
 
 
+@pytest.mark.parametrize("D,page", [(64, 32), (128, 16), (128, 128)])
+@pytest.mark.parametrize("new", [1, 7, 140])
+def test_scales_that_are_no_powers_of_two(D, page, new):
+    """A pool that something else filled: any codes but NaN, any positive scales."""
+    s = Setup([333, 150], [new, new], 2, D, "fp8", page)
+    g = torch.Generator(device="cuda").manual_seed(new)
+    for name in ("k", "v"):
+        codes = torch.randint(0, 127, s.cache.k.shape, generator=g, device="cuda") + \
+            128 * torch.randint(0, 2, s.cache.k.shape, generator=g, device="cuda")
+        getattr(s.cache, name).copy_(codes.to(torch.uint8))
+        getattr(s.cache, name + "_scale").copy_(0.003 + 0.01 * torch.rand(s.cache.k.shape[:2], generator=g, device="cuda"))
+    s.take()
+    # rounding V's code times the scale's mantissa to fp16 is the bound's weight rounding once more
+    attention(s, 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_many_sequences_and_many_heads(dtype):
+    """300 sequences of 0 to 40 tokens; 128 query heads on one K/V head."""
+    r = np.random.default_rng(5)
+    lens = [int(n) for n in r.integers(0, 41, 300)]
+    s = Setup(lens, [min(1, n) for n in lens], 1, 64, dtype, 16, garbage=True)
+    s.fill(2)
+    attention(s, 3, window=9, n_sink=2)
+    for new in (1, 3):
+        s = Setup([90], [new], 1, 128, dtype, 32, garbage=True)
+        s.fill(3)
+        attention(s, 128, slopes=[0.01 * h for h in range(128)])
+
+
+def test_calls_from_two_threads():
+    """One batch and cache, two threads with row counts of their own."""
+    import threading
+    s = Setup([500, 400], [1, 1], 2, 64, "fp8", 16)
+    s.fill(2)
+    b = s.batch()
+    qs = [torch.randn((n, 4, 64), device="cuda").bfloat16() for n in (2, 5)]
+    want = [swa.paged_attention(q, s.cache, b)[:2].clone() for q in qs]
+    bad = []
+
+    def work(q, w):
+        st = torch.cuda.Stream()
+        for _ in range(50):
+            with torch.cuda.stream(st):
+                got = swa.paged_attention(q, s.cache, b)
+                st.synchronize()
+                if not torch.equal(got[:2], w):
+                    bad.append(1)
+
+    torch.cuda.synchronize()
+    ts = [threading.Thread(target=work, args=a) for a in zip(qs, want)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not bad
+
+
 def test_bounds_of_the_host_hold_on_the_device():
     """Arrays that say more than the host's bounds: rows beyond max_q and total_q are
     not processed, keys beyond max_kv and the table do not exist."""

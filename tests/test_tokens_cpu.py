@@ -182,7 +182,8 @@ def test_attention_refusals(L):
                     (dict(stride=32 * 128 + 4), "stride"), (dict(dt=swa.LL_F32), "BF16"), (dict(Hq=12), "multiple"),
                     (dict(Hq=0), "multiple"), (dict(scores=sc(-1.0)), "softmax_scale"),
                     (dict(scores=sc(float("inf"))), "softmax_scale"), (dict(scores=sc(0.0, -2.0)), "soft_cap"),
-                    (dict(scores=sc(0.0, float("nan"))), "soft_cap"), (dict(scores=sc(0.0, 0.0, -1)), "window"),
+                    (dict(scores=sc(0.0, float("nan"))), "soft_cap"),
+                    (dict(scores=sc(0.0, 1e-44)), "range"), (dict(scores=sc(3e38)), "range"), (dict(scores=sc(0.0, 0.0, -1)), "window"),
                     (dict(scores=sc(0.0, 0.0, 0, -1)), "n_sink"), (dict(scores=sc(0.0, 0.0, 0, 0, A + 2)), "prefix_len"),
                     (dict(scores=slopes), "slopes[31]"), (dict(batch=long, ws_bytes=16), "workspace"),
                     (dict(batch=long, ws=None), "workspace"), (dict(batch=long, ws=A + 4), "workspace")]:
@@ -219,6 +220,21 @@ def test_workspace_is_zero_for_short_histories_and_bad_descriptors(L):
     assert ws(_cache(), _batch(max_kv=200000, max_pages=20000), 32) > 0
     assert ws(_cache(), _batch(total_q=0), 32) == 0
     assert ws(_cache(D=96), _batch(), 32) == 0 and ws(_cache(), _batch(B=0), 32) == 0 and ws(_cache(), _batch(), 12) == 0
+
+
+def test_pool_bound_and_kept_descriptors(L):
+    refused(L, _append(L, cache=_cache(n_pages=1 << 29, H=8)), "2^31 - 1")
+    import torch
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    batch = swa.TokenBatch(i32(3), i32(2), i32(2, 4), 1, 64)
+    cache = swa.PagedKVCache(4, 16, 2, 64, "fp8", device="cpu")
+    a = cache.to_c()
+    assert cache.to_c() is a and (a.n_pages, a.page_size, a.H, a.D, a.dtype) == (4, 16, 2, 64, swa.LL_FP8_E4M3)
+    cache.k = cache.k.clone()  # another tensor: another descriptor, the old one left as it was
+    b = cache.to_c()
+    assert b is not a and b.k == cache.k.data_ptr() and a.k != b.k and b.v == a.v
+    with pytest.raises(ValueError, match="CUDA"):
+        batch.to_c(2, 0)
 
 
 def test_binding_refusals(L):
