@@ -139,7 +139,8 @@ struct AttnPlan {
   int row_tile, key_tile, row_tiles, chunk, nsplit;
 };
 
-AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq) {
+// The plan for key ranges of at most `span` keys (0: no such bound).
+AttnPlan plan_for_span(const ll_paged_cache* c, const ll_token_batch* t, int Hq, long long span) {
   AttnPlan a;
   const int group = Hq / c->H;
   const long long max_q = t->max_q < t->total_q ? t->max_q : t->total_q;
@@ -147,8 +148,9 @@ AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq
   a.row_tile = a.tiles ? 256 : (max_q * group <= 8 ? 8 : 16);
   a.key_tile = a.tiles ? 128 : 16;
   a.row_tiles = static_cast<int>((max_q * group + a.row_tile - 1) / a.row_tile);
-  // at most (window and prefix only shorten a range)
-  const long long keys = max_key(t, c->page_size);
+  long long keys = max_key(t, c->page_size);
+  // a span's ends and the sinks' end may each cut a tile
+  if (span > 0 && span + 3 * a.key_tile < keys) keys = span + 3 * a.key_tile;
   const long long nt = keys > 0 ? (keys + a.key_tile - 1) / a.key_tile : 1;
   const long long units = static_cast<long long>(t->B) * c->H * (a.row_tiles > 0 ? a.row_tiles : 1);
   long long chunk = nt;
@@ -194,6 +196,17 @@ size_t paged_workspace(const AttnPlan& a, const ll_token_batch* t, int Hq, int D
   if (a.nsplit <= 1 || a.clustered) return 0;
   return align256(static_cast<size_t>(t->total_q) * Hq * a.nsplit * D * sizeof(float)) +
          align256(static_cast<size_t>(t->total_q) * Hq * a.nsplit * sizeof(float2));
+}
+
+// A window shortens every range to itself, the positions of a unit's rows and the sinks
+// (a prefix may be of any length). The workspace is sized without it, so its plan is
+// taken where it needs no more.
+AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq, const ll_score_desc* sc) {
+  const AttnPlan a = plan_for_span(c, t, Hq, 0);
+  if (sc->window == 0 || sc->prefix_len != nullptr) return a;
+  const long long rows = a.row_tile / (Hq / c->H) + 2;
+  const AttnPlan w = plan_for_span(c, t, Hq, static_cast<long long>(sc->window) + sc->n_sink + rows);
+  return paged_workspace(w, t, Hq, c->D) <= paged_workspace(a, t, Hq, c->D) ? w : a;
 }
 
 template <class TR, int MODS>
@@ -396,7 +409,7 @@ size_t ll_paged_attention_workspace_bytes(const ll_paged_cache* cache, const ll_
   if (check_paged_cache(cache) != LL_OK || check_batch(batch) != LL_OK || Hq < 1 || Hq % cache->H != 0 ||
       Hq > LL_MAX_TOKEN_HEADS)
     return 0;
-  return paged_workspace(plan_attention(cache, batch, Hq), batch, Hq, cache->D);
+  return paged_workspace(plan_for_span(cache, batch, Hq, 0), batch, Hq, cache->D);
 }
 
 ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype, int Hq, const ll_paged_cache* cache,
@@ -439,7 +452,7 @@ ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype
       if (!std::isfinite(p.sc.slope2[h])) return fail(LL_ERR_INVALID_ARG, "slopes[%d] leaves fp32's range", h);
     }
   }
-  const AttnPlan plan = plan_attention(cache, batch, Hq);
+  const AttnPlan plan = plan_attention(cache, batch, Hq, sc);
   const size_t need = paged_workspace(plan, batch, Hq, cache->D);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return fail(LL_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);

@@ -89,9 +89,13 @@ __device__ __forceinline__ void unit_positions(const PagedAttnParams& p, const S
   hi = s.first_pos + last / p.group;
 }
 
+// Pieces of a range of nt tiles, and the end of one: the host's bounds on ranges make
+// nsplit enough; the last piece takes what they should have missed.
 __device__ __forceinline__ int piece_count(const PagedAttnParams& p, int nt) {
-  const int n = (nt + p.chunk - 1) / p.chunk;
-  return n > 1 ? n : 1;
+  return max(1, min((nt + p.chunk - 1) / p.chunk, p.nsplit));
+}
+__device__ __forceinline__ int piece_end(int split, int pieces, int chunk, int nt) {
+  return split == pieces - 1 ? nt : min(nt, (split + 1) * chunk);
 }
 
 // What a kernel is compiled for beyond a scaled product: a branch per score, or the
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunk = p.clustered ? (kr.nt + pieces - 1) / pieces : p.chunk;
   const int t_beg = split * chunk + warp;
-  const int t_end = min(kr.nt, (split + 1) * chunk);
+  const int t_end = piece_end(split, pieces, chunk, kr.nt);
   const int n_my = t_end > t_beg ? (t_end - t_beg + NW - 1) / NW : 0;
 
   // ---- the ring

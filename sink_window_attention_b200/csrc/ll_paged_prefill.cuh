@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
   const int pieces = piece_count(p, kr.nt);
   if (split >= pieces) return;
   const int t_beg = split * p.chunk;
-  const int n = min(kr.nt, t_beg + p.chunk) - t_beg;  // key tiles of this piece (0: nothing is seen)
+  const int n = piece_end(split, pieces, p.chunk, kr.nt) - t_beg;  // key tiles of this piece (0: nothing is seen)
   const bool two = rows - r0 > BM;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
