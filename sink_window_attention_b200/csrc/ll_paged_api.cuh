@@ -122,6 +122,12 @@ ll_status allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
 // 2000-8000 keys, 8-bit: 48 rows 64 us (tiles of 128 rows: 89), 64 rows 81 (92), 96 rows
 // 109 (94); bf16: 48 rows 70 (81), 64 rows 89 (83).
 constexpr int kDecodeRows = 48;
+// Over short ranges, which stay in L2, it is taken for more rows where its waves of
+// blocks (6 us to start and end one, 0.08 us per 16 keys of 128 elements) take less than
+// the tile kernel's (10 us, 2.4 us per 128 keys). 1000 keys, decode (tiles): one sequence,
+// 8 K/V heads of 128, 512 rows 21 us (27), 1024 rows 38 (34); six, 256 rows 23 (35), 512
+// rows 40 (33); six, 12 heads of 64, 256 rows 25 (36), 512 rows 30 (26).
+constexpr long long kShortRange = 1024;
 
 // Blocks of the decode kernel that an SM holds.
 int decode_blocks(const ll_paged_cache* c, int rows) {
@@ -144,28 +150,40 @@ AttnPlan plan_for_span(const ll_paged_cache* c, const ll_token_batch* t, int Hq,
   AttnPlan a;
   const int group = Hq / c->H;
   const long long max_q = t->max_q < t->total_q ? t->max_q : t->total_q;
-  a.tiles = max_q * group > kDecodeRows;
-  a.row_tile = a.tiles ? 256 : (max_q * group <= 8 ? 8 : 16);
+  const long long rows = max_q * group, keys = max_key(t, c->page_size);
+  // tiles in a range at most: a span's two ends and the sinks' end may each cut one
+  auto tiles_of = [&](long long tile) {
+    const long long n = span > 0 && span + 3 * tile < keys ? span + 3 * tile : keys;
+    return n > 0 ? (n + tile - 1) / tile : 1;
+  };
+  auto waves_of = [&](long long row_tile, long long slots) {
+    return ((rows + row_tile - 1) / row_tile * t->B * c->H + slots - 1) / slots;
+  };
+  a.tiles = rows > kDecodeRows;
+  if (a.tiles && 16 * tiles_of(16) <= kShortRange)
+    a.tiles = waves_of(256, num_sms()) * (1000 + 240 * tiles_of(128)) <
+              waves_of(16, 3ll * num_sms()) * (600 + 8 * tiles_of(16) * c->D / 128);
+  a.row_tile = a.tiles ? 256 : (rows <= 8 ? 8 : 16);
   a.key_tile = a.tiles ? 128 : 16;
-  a.row_tiles = static_cast<int>((max_q * group + a.row_tile - 1) / a.row_tile);
-  long long keys = max_key(t, c->page_size);
-  // a span's ends and the sinks' end may each cut a tile
-  if (span > 0 && span + 3 * a.key_tile < keys) keys = span + 3 * a.key_tile;
-  const long long nt = keys > 0 ? (keys + a.key_tile - 1) / a.key_tile : 1;
+  a.row_tiles = static_cast<int>((rows + a.row_tile - 1) / a.row_tile);
+  const long long nt = tiles_of(a.key_tile);
   const long long units = static_cast<long long>(t->B) * c->H * (a.row_tiles > 0 ? a.row_tiles : 1);
   long long chunk = nt;
   if (!a.tiles) {
-    // whole waves of blocks, so that equal lengths leave no block over, and several,
-    // so that ragged ones even out; (one sequence is as long as
-    // itself: one wave); no piece below 128 keys (two tiles per warp). Up to 8 blocks (the
-    // portable cluster) join on chip, more through the workspace.
+    // Long ranges: three waves of blocks, whole ones so that equal lengths leave no block
+    // over, several so that ragged ones even out (one sequence is as long as itself: one
+    // wave). Where that leaves less than 512 keys to a piece the join would cost more than
+    // it saves, and latency counts: no more blocks than run at once, at least 128 keys
+    // each (two tiles per warp), in a cluster (8 blocks are portable) where they fit one.
     const long long slots = decode_blocks(c, a.row_tile) * static_cast<long long>(num_sms());
-    const long long pieces = (t->B > 1 ? 3 : 1) * slots / units;
-    chunk = pieces > 1 ? (nt + pieces - 1) / pieces : nt;
-    if (chunk < 8) chunk = 8;
-    if ((nt + chunk - 1) / chunk > 8) {
-      if (nt <= 8 * 16) chunk = (nt + 7) / 8;  // up to 256 keys each: rather a cluster
-      else if (chunk < 24) chunk = 24;
+    const long long many = (t->B > 1 ? 3 : 1) * slots / units, few = slots / units;
+    if (many > 1 && nt >= 32 * many) {
+      chunk = (nt + many - 1) / many;
+    } else {
+      long long pieces = nt / 8 < few ? nt / 8 : few;
+      if (pieces > 8 && (pieces <= 12 || nt <= 8 * 16)) pieces = 8;
+      if (pieces > 8 && nt < 24 * pieces) pieces = nt / 24 > 8 ? nt / 24 : 8;
+      chunk = pieces > 1 ? (nt + pieces - 1) / pieces : nt;
     }
   } else {
     // one block per SM: the number of pieces with the least waves x tiles. A block's start
@@ -204,7 +222,7 @@ size_t paged_workspace(const AttnPlan& a, const ll_token_batch* t, int Hq, int D
 AttnPlan plan_attention(const ll_paged_cache* c, const ll_token_batch* t, int Hq, const ll_score_desc* sc) {
   const AttnPlan a = plan_for_span(c, t, Hq, 0);
   if (sc->window == 0 || sc->prefix_len != nullptr) return a;
-  const long long rows = a.row_tile / (Hq / c->H) + 2;
+  const long long rows = 256 / (Hq / c->H) + 2;
   const AttnPlan w = plan_for_span(c, t, Hq, static_cast<long long>(sc->window) + sc->n_sink + rows);
   return paged_workspace(w, t, Hq, c->D) <= paged_workspace(a, t, Hq, c->D) ? w : a;
 }
