@@ -526,7 +526,8 @@ typedef struct ll_score_desc {
  * Keys that no query of a tile of rows sees are not read, so what their places
  * hold does not matter; a NaN or infinity in a key or value that some query of
  * the call sees may spoil the call's other rows of that sequence too.
- * Over a BF16 pool the rotated q and the softmax weights are rounded to bf16;
+ * Over a BF16 pool the softmax weights are rounded to bf16, and the rotated q to bf16
+ * (calls of more than a few rows) or to two bf16 terms;
  * over an FP8 pool codes are used exactly, q and weights are rounded to fp16
  * under a power-of-two scale. Sums, maxima and outputs before the last rounding
  * are fp32.
@@ -537,7 +538,8 @@ typedef struct ll_score_desc {
  * a q_stride that is no multiple of 8 or < Hq * D, a negative or non-finite
  * softmax_scale or soft_cap (or a quotient of them outside fp32's range), negative
  * window or n_sink, a slope that is not finite, a workspace that is too small;
- * LL_ERR_UNSUPPORTED for Hq > LL_MAX_TOKEN_HEADS or more than 2^31 - 1 blocks.
+ * LL_ERR_UNSUPPORTED for Hq > LL_MAX_TOKEN_HEADS, for max_q * Hq / H > 256 * 65535
+ * and for more than 2^31 - 1 blocks.
  */
 size_t ll_paged_attention_workspace_bytes(const ll_paged_cache* cache, const ll_token_batch* batch, int Hq);
 

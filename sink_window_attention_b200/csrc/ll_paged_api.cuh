@@ -254,7 +254,7 @@ ll_status launch_paged_prefill(const ll::PagedAttnParams& p, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   ll_status st = allow_smem(kern, TR::SMEM, done);
   if (st != LL_OK) return st;
-  kern<<<dim3(p.nsplit * p.row_tiles, p.pool.H, p.batch.B), TR::THREADS, TR::SMEM, s>>>(p);
+  kern<<<dim3(p.nsplit * p.pool.H, p.batch.B, p.row_tiles), TR::THREADS, TR::SMEM, s>>>(p);
   return check_launch("paged_prefill_kernel");
 }
 
@@ -498,6 +498,8 @@ ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype
   if (p.batch.max_q == 0) return LL_OK;
   if (static_cast<long long>(p.nsplit) * p.row_tiles > INT_MAX || static_cast<long long>(p.batch.max_q) * Hq > INT_MAX)
     return fail(LL_ERR_UNSUPPORTED, "the call needs more than 2^31 - 1 blocks");
+  if (plan.tiles && p.row_tiles > 65535)
+    return fail(LL_ERR_UNSUPPORTED, "max_q x Hq / H = %lld exceeds 256 x 65535", static_cast<long long>(p.batch.max_q) * p.group);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->dtype == LL_FP8_E4M3;
   if (cache->D == 128)

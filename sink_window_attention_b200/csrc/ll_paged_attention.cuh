@@ -208,6 +208,11 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t& lo, uint32_t
 //  * O^T: P leaves S^T with keys along lanes g and is turned by two 8 x 8 transposes;
 //    the lane reads the V rows of keys 2t, 2t+1, 2t+8, 2t+9 at chunk g (+ 8), and
 //    byte permutes pair two keys at the same d.
+// One query per sequence, 8 K/V heads of 128: 4 sequences of up to 131000 keys (64 query
+// heads, 8-bit pool, 701 MB) 127 us, 5.5 TB/s, 84 % of a copy's rate; 48 of 2000 to 8000
+// (472 MB) 94 us, 5.0 TB/s; bf16 pool, the same 48 (945 MB) 153 us, 6.2 TB/s. With query
+// rows as the MMA's 16 rows the 8-bit batch took 110 us, with a conversion per E4M3 pair
+// that unpacked its operand 178 us.
 // ---------------------------------------------------------------------------
 template <int D_, bool E4M3_, int ROWS_>
 struct DecodeTraits {
@@ -232,7 +237,8 @@ struct DecodeTraits {
   // with 3 stages each read 5.6 TB/s, 3 with 4 stages 4.4, 4 with 2 stages 5.4.
   static constexpr int BLOCKS = ROWB >= 256 ? 2 : (ROWS == 8 ? 4 : 3);
   static constexpr int META = NW * STAGES * 16;
-  static constexpr int SMEM = RING + META + ROWS * QP * 2 + ROWS * 4 + 2 * NW * ROWS * 4;
+  static constexpr int QS = E4M3 ? 1 : 2;   // terms of Q
+  static constexpr int SMEM = RING + META + QS * ROWS * QP * 2 + ROWS * 4 + 2 * NW * ROWS * 4;
   static_assert((NW + 1) * ROWS * D * 4 <= RING, "the warps' O and their sum must fit the ring");
 };
 
@@ -271,8 +277,8 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* s_ring = smem;
   float* s_meta = reinterpret_cast<float*>(smem + TR::RING);  // [NW][STAGES][4]: K scale, V scale, page mapped
-  uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + TR::RING + TR::META);  // [ROWS][QP]
-  float* s_qf = reinterpret_cast<float*>(s_q + ROWS * TR::QP);              // [ROWS]
+  uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + TR::RING + TR::META);  // [QS][ROWS][QP]
+  float* s_qf = reinterpret_cast<float*>(s_q + TR::QS * ROWS * TR::QP);     // [ROWS]
   float* s_m = s_qf + ROWS;                                                 // [NW][ROWS]
   float* s_l = s_m + NW * ROWS;
 
@@ -378,11 +384,20 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
       }
       if (c == 0) s_qf[r] = f;
     } else {
+      // two bf16 terms: a rotated q keeps 16 bits, for MMAs that the loads hide (one
+      // term: error 3.5e-3 of the output, two: 2.2e-3, of which 1.7e-3 is its rounding)
+      uint32_t v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-        w[4 + e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+      for (int e = 0; e < 8; ++e) {
+        const float a = e < 4 ? x[2 * (e & 3)] : y[2 * (e & 3)], b2 = e < 4 ? x[2 * (e & 3) + 1] : y[2 * (e & 3) + 1];
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b2);
+        const float2 f2 = __bfloat1622float2(h2);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+        v[e] = pack_bf16(a - f2.x, b2 - f2.y);
       }
+      uint16_t* s_lo = s_q + ROWS * TR::QP + r * TR::QP;
+      *reinterpret_cast<uint4*>(s_lo + lo * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4*>(s_lo + hi * 8) = make_uint4(v[4], v[5], v[6], v[7]);
       if (c == 0) s_qf[r] = 1.f;
     }
     *reinterpret_cast<uint4*>(s_q + r * TR::QP + lo * 8) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -466,8 +481,17 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int r = 0; r < NR; ++r)
-            mma16816<false>(e & 1 ? sy[r] : sx[r], ua[2 * e], wa[2 * e], ua[2 * e + 1], wa[2 * e + 1], bq[r][i * 2 + e][0],
-                            bq[r][i * 2 + e][1]);
+            mma16816<false>(e & 1 ? sy[r] : sx[r], ua[2 * e], wa[2 * e], ua[2 * e + 1], wa[2 * e + 1],
+                            bq[r][i * 2 + e][0], bq[r][i * 2 + e][1]);
+        if (p.rope.rot > 0) {  // an unrotated q is bf16 as it stands
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const uint2 q2 = *reinterpret_cast<const uint2*>(s_q + (ROWS + g + 8 * r) * TR::QP + (t + 4 * i) * 8 + 4 * e);
+              mma16816<false>(e & 1 ? sx[r] : sy[r], ua[2 * e], wa[2 * e], ua[2 * e + 1], wa[2 * e + 1], q2.x, q2.y);
+            }
+        }
       }
     }
     // scores in log2 units
@@ -591,7 +615,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   __syncthreads();
   float* s_o = reinterpret_cast<float*>(s_ring);  // [NW][ROWS][D]
   float* c_o = s_o + NW * ROWS * D;               // [ROWS][D]: the block's sum, for its cluster
-  float2* c_ml = reinterpret_cast<float2*>(s_q);  // [ROWS]
+  float2* c_ml = reinterpret_cast<float2*>(s_q);  // [ROWS]: Q is done with
 #pragma unroll
   for (int q = 0; q < 2 * NR; ++q) {
     const int row = 2 * t + (q & 1) + 8 * (q >> 1);

@@ -19,6 +19,11 @@
 //  * warps 8-11 and 12-15 are A's and B's softmax, a row per thread: maxima and
 //    sums in fp32; O is rescaled in tensor memory only when the reference is
 //    exceeded by 2^8.
+// 1024 queries of 32 heads over 32768 keys (8 K/V heads of 128, 128 CTAs): 565 us, 958
+// TFLOP/s, over a bf16 pool, 660 us over an 8-bit one (its softmax reads the groups' scales
+// and has 4 operand buffers instead of 5). Per 256 x 128 tile about 4000 clocks: 2048 of
+// MMAs, 2048 of exponentials, and what one softmax warp per row tile and scheduler cannot
+// overlap. A CTA takes about 6 us to start (lengths, pages, Q, first tiles) and end.
 // 8-bit pools: a group of 16 keys lies in one page, so its K scale is a factor and
 // the exponent of its V scale an offset per 16 scores; the V scale's mantissa (1
 // for the powers of two that the append writes) is multiplied into V's fp16.
@@ -123,9 +128,9 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
   static_assert((8 + 8 + TR::META + 10) * 8 + 8 + TR::META * 4 <= 512 && 512 + TR::META * 8 * sizeof(KeyGroup) <= TR::CTRL, "control block");
 
   asm volatile("griddepcontrol.launch_dependents;");
-  // the last rows of a sequence see the most keys: they start first
-  const int rt = p.row_tiles - 1 - blockIdx.x % p.row_tiles, split = blockIdx.x / p.row_tiles;
-  const int hkv = blockIdx.y, b = blockIdx.z;
+  // the last rows of a sequence see the most keys: those of all sequences start first
+  const int hkv = blockIdx.x % p.pool.H, split = blockIdx.x / p.pool.H;
+  const int b = blockIdx.y, rt = p.row_tiles - 1 - blockIdx.z;
   const int ps = p.pool.page_size;
   const SeqView s = seq_view(p.batch, b);
   const int rows = s.nq * p.group, r0 = rt * 2 * BM;
