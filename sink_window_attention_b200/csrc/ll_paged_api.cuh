@@ -142,7 +142,7 @@ int decode_blocks(const ll_paged_cache* c, int rows) {
 struct AttnPlan {
   bool tiles;      // 128-row tensor-memory tiles; else warp tiles of 8 or 16 rows
   bool clustered;  // the pieces of a unit are joined by a cluster on chip; else through the workspace
-  int row_tile, key_tile, row_tiles, chunk, nsplit;
+  int row_tile, key_tile, row_tiles, chunk, chunk0, nsplit;
 };
 
 // The plan for key ranges of at most `span` keys (0: no such bound).
@@ -168,7 +168,7 @@ AttnPlan plan_for_span(const ll_paged_cache* c, const ll_token_batch* t, int Hq,
   a.row_tiles = static_cast<int>((rows + a.row_tile - 1) / a.row_tile);
   const long long nt = tiles_of(a.key_tile);
   const long long units = static_cast<long long>(t->B) * c->H * (a.row_tiles > 0 ? a.row_tiles : 1);
-  long long chunk = nt;
+  long long chunk = nt, chunk0 = 0;  // chunk0 0: like the others
   if (!a.tiles) {
     // Long ranges: three waves of blocks, whole ones so that equal lengths leave no block
     // over, several so that ragged ones even out (one sequence is as long as itself: one
@@ -200,9 +200,21 @@ AttnPlan plan_for_span(const ll_paged_cache* c, const ll_token_batch* t, int Hq,
         chunk = per;
       }
     }
+    // fewer units than SMs: the SMs left over take the ends of all ranges, in as many
+    // rounds as it takes, while the units' own blocks do the rest
+    const long long spare = num_sms() - units;
+    if (spare > 0) {
+      const long long rounds = (units + spare - 1) / spare;
+      const long long end = (nt + 3 - 3 * rounds) / (rounds + 1);
+      if (end > 0 && 100 * (nt - end + 3) + 200 + 2 * piece_bytes / 160000 < best) {
+        chunk = end;
+        chunk0 = nt - end;
+      }
+    }
   }
   a.chunk = static_cast<int>(chunk < nt ? chunk : nt);
-  a.nsplit = static_cast<int>((nt + a.chunk - 1) / a.chunk);
+  a.chunk0 = static_cast<int>(chunk0 > 0 ? chunk0 : a.chunk);
+  a.nsplit = chunk0 > 0 ? 2 : static_cast<int>((nt + a.chunk - 1) / a.chunk);
   // where all blocks run at once latency counts; in several waves a cluster's blocks wait
   // for one another's places (batch of 48: 95 us clustered, 91 us not)
   a.clustered = !a.tiles && a.nsplit > 1 && a.nsplit <= 8 &&
@@ -254,7 +266,7 @@ ll_status launch_paged_prefill(const ll::PagedAttnParams& p, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   ll_status st = allow_smem(kern, TR::SMEM, done);
   if (st != LL_OK) return st;
-  kern<<<dim3(p.nsplit * p.pool.H, p.batch.B, p.row_tiles), TR::THREADS, TR::SMEM, s>>>(p);
+  kern<<<dim3(p.pool.H, p.batch.B, p.row_tiles * p.nsplit), TR::THREADS, TR::SMEM, s>>>(p);
   return check_launch("paged_prefill_kernel");
 }
 
@@ -487,6 +499,7 @@ ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype
   p.key_tile = plan.key_tile;
   p.row_tiles = plan.row_tiles;
   p.chunk = plan.chunk;
+  p.chunk0 = plan.chunk0;
   p.nsplit = plan.nsplit;
   p.clustered = plan.clustered;
   if (need > 0) {
@@ -498,8 +511,9 @@ ll_status ll_paged_attention(const void* q, long long q_stride, ll_dtype q_dtype
   if (p.batch.max_q == 0) return LL_OK;
   if (static_cast<long long>(p.nsplit) * p.row_tiles > INT_MAX || static_cast<long long>(p.batch.max_q) * Hq > INT_MAX)
     return fail(LL_ERR_UNSUPPORTED, "the call needs more than 2^31 - 1 blocks");
-  if (plan.tiles && p.row_tiles > 65535)
-    return fail(LL_ERR_UNSUPPORTED, "max_q x Hq / H = %lld exceeds 256 x 65535", static_cast<long long>(p.batch.max_q) * p.group);
+  if (plan.tiles && static_cast<long long>(p.row_tiles) * p.nsplit > 65535)
+    return fail(LL_ERR_UNSUPPORTED, "max_q x Hq / H = %lld exceeds 256 x 65535 rows",
+                static_cast<long long>(p.batch.max_q) * p.group);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->dtype == LL_FP8_E4M3;
   if (cache->D == 128)

@@ -37,6 +37,7 @@ struct PagedAttnParams {
   int row_tile;      // rows (token, query head of the group) of a unit
   int key_tile;      // keys per step; pieces begin at multiples of it
   int chunk;         // key tiles per piece
+  int chunk0;        // and of the first piece, which may be longer
   int nsplit;        // pieces at most
   int clustered;     // decode: the nsplit blocks of a unit form a cluster, share its keys evenly and join on chip
   int row_tiles;     // units of a sequence and K/V head at most
@@ -89,13 +90,16 @@ __device__ __forceinline__ void unit_positions(const PagedAttnParams& p, const S
   hi = s.first_pos + last / p.group;
 }
 
-// Pieces of a range of nt tiles, and the end of one: the host's bounds on ranges make
-// nsplit enough; the last piece takes what they should have missed.
+// Pieces of a range of nt tiles, and where one begins and ends: the host's bounds on
+// ranges make nsplit enough; the last piece takes what they should have missed.
 __device__ __forceinline__ int piece_count(const PagedAttnParams& p, int nt) {
-  return max(1, min((nt + p.chunk - 1) / p.chunk, p.nsplit));
+  return nt <= p.chunk0 ? 1 : min(1 + (nt - p.chunk0 + p.chunk - 1) / p.chunk, p.nsplit);
 }
-__device__ __forceinline__ int piece_end(int split, int pieces, int chunk, int nt) {
-  return split == pieces - 1 ? nt : min(nt, (split + 1) * chunk);
+__device__ __forceinline__ int piece_begin(const PagedAttnParams& p, int split) {
+  return split == 0 ? 0 : p.chunk0 + (split - 1) * p.chunk;
+}
+__device__ __forceinline__ int piece_end(const PagedAttnParams& p, int split, int pieces, int nt) {
+  return split == pieces - 1 ? nt : min(nt, piece_begin(p, split + 1));
 }
 
 // What a kernel is compiled for beyond a scaled product: a branch per score, or the
@@ -295,9 +299,10 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   const int pieces = p.clustered ? p.nsplit : piece_count(p, kr.nt);
   if (split >= pieces) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int chunk = p.clustered ? (kr.nt + pieces - 1) / pieces : p.chunk;
-  const int t_beg = split * chunk + warp;
-  const int t_end = piece_end(split, pieces, chunk, kr.nt);
+  // a cluster shares its unit's keys evenly
+  const int even = (kr.nt + pieces - 1) / pieces;
+  const int t_beg = (p.clustered ? split * even : piece_begin(p, split)) + warp;
+  const int t_end = p.clustered ? min(kr.nt, (split + 1) * even) : piece_end(p, split, pieces, kr.nt);
   const int n_my = t_end > t_beg ? (t_end - t_beg + NW - 1) / NW : 0;
 
   // ---- the ring

@@ -19,9 +19,10 @@
 //  * warps 8-11 and 12-15 are A's and B's softmax, a row per thread: maxima and
 //    sums in fp32; O is rescaled in tensor memory only when the reference is
 //    exceeded by 2^8.
-// 1024 queries of 32 heads over 32768 keys (8 K/V heads of 128, 128 CTAs): 565 us, 958
-// TFLOP/s, over a bf16 pool, 660 us over an 8-bit one (its softmax reads the groups' scales
-// and has 4 operand buffers instead of 5). Per 256 x 128 tile about 4000 clocks: 2048 of
+// 1024 queries of 32 heads over 32768 keys (8 K/V heads of 128): 551 us, 980 TFLOP/s, over a
+// bf16 pool, 642 us over an 8-bit one (its softmax reads the groups' scales and has 4
+// operand buffers instead of 5); without the ranges' ends on the SMs that 128 units leave
+// over, 565 and 655. Per 256 x 128 tile about 4000 clocks: 2048 of
 // MMAs, 2048 of exponentials, and what one softmax warp per row tile and scheduler cannot
 // overlap. A CTA takes about 6 us to start (lengths, pages, Q, first tiles) and end.
 // 8-bit pools: a group of 16 keys lies in one page, so its K scale is a factor and
@@ -129,8 +130,9 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
 
   asm volatile("griddepcontrol.launch_dependents;");
   // the last rows of a sequence see the most keys: those of all sequences start first
-  const int hkv = blockIdx.x % p.pool.H, split = blockIdx.x / p.pool.H;
-  const int b = blockIdx.y, rt = p.row_tiles - 1 - blockIdx.z;
+  // (and a range's first piece, which may be the longer, before the others)
+  const int hkv = blockIdx.x, b = blockIdx.y;
+  const int split = blockIdx.z / p.row_tiles, rt = p.row_tiles - 1 - blockIdx.z % p.row_tiles;
   const int ps = p.pool.page_size;
   const SeqView s = seq_view(p.batch, b);
   const int rows = s.nq * p.group, r0 = rt * 2 * BM;
@@ -140,8 +142,8 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
   const KeyRange kr = key_range(p.sc, b, s, p_lo, p_hi, BN);
   const int pieces = piece_count(p, kr.nt);
   if (split >= pieces) return;
-  const int t_beg = split * p.chunk;
-  const int n = piece_end(split, pieces, p.chunk, kr.nt) - t_beg;  // key tiles of this piece (0: nothing is seen)
+  const int t_beg = piece_begin(p, split);
+  const int n = piece_end(p, split, pieces, kr.nt) - t_beg;  // key tiles of this piece (0: nothing is seen)
   const bool two = rows - r0 > BM;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -547,8 +549,17 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
             for (int e = 0; e < 32; ++e) sr[c][e] = seen & (1u << e) ? sr[c][e] : __float_as_uint(-INFINITY);
           }
         }
-        // factor on the scores of group g (kept off 0, so that masked ones stay -inf)
-        auto factor = [&](int g) { return MODS != 0 ? 1.f : (E4M3 ? fmaxf(fac * kg[g].ks, 1e-37f) : fac); };
+        // factors on the scores of the groups (kept off 0, so that masked ones stay -inf)
+        // and the exponents of their V scales, read once
+        float fg[8], cg[8];
+        if constexpr (E4M3)
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float2 u = *reinterpret_cast<const float2*>(kg + g);  // ks, c
+            fg[g] = MODS != 0 ? 1.f : fmaxf(fac * u.x, 1e-37f);
+            cg[g] = u.y;
+          }
+        const float f_all = MODS != 0 ? 1.f : fac;  // bf16: one factor
         float mg[8];  // maxima of the groups, chains of their own
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
@@ -559,10 +570,10 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
             q[e] = fmax3(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
                          fmaxf(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])));
           mg[g] = fmaxf(fmax3(q[0], q[1], q[2]), q[3]);
-          if (E4M3) mg[g] = fmaf(mg[g], factor(g), kg[g].c);
+          if constexpr (E4M3) mg[g] = fmaf(mg[g], fg[g], cg[g]);
         }
         float mx = fmaxf(fmax3(fmax3(mg[0], mg[1], mg[2]), mg[3], mg[4]), fmax3(mg[5], mg[6], mg[7]));
-        if (!E4M3) mx *= factor(0);
+        if (!E4M3) mx *= f_all;
         const bool raise = mx > m + 8.f;
         const float m_use = raise ? mx : m;
         // S_i complete implies that P V i - 1, issued before it, is
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int g = 2 * c + hf;
-            const float f = factor(g), off = E4M3 ? kg[g].c - ms : -ms;
+            const float f = E4M3 ? fg[g] : f_all, off = E4M3 ? cg[g] - ms : -ms;
             const uint64_t f2 = f2_pack(f, f), off2 = f2_pack(off, off);
             uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
