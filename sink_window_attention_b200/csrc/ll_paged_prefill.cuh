@@ -321,7 +321,6 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
 #pragma unroll
           for (int k = 0; k < STEPS; ++k)
             buf[k] = *reinterpret_cast<const uint4*>(sRaw + (kv * STEPS + k) * 2048 + tid * 16);
-          fetch(kv, i + 1, run1);
           wait_empty(st, round);
           if (!ok) break;
           uint8_t* dst = sKV + st * TILE;
@@ -344,6 +343,8 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
           }
           if (kv == 0) put_meta(i);
           publish(st);
+          // the copy into a place that was just read: behind the reads' last use
+          fetch(kv, i + 1, run1);
           if (++st == STAGES) st = 0, ++round;
         }
         pg = pg1;
