@@ -140,6 +140,16 @@ __device__ __forceinline__ float scale_exponent(float s) {
   return static_cast<float>(e < -60 ? -60 : (e > 60 ? 60 : e));
 }
 
+// The running reference of a row's exponents is raised where a score exceeds it by 2^8,
+// so a weight is at most 2^8. bf16 weights keep their 8 bits however small they are. fp16
+// ones (8-bit pools) are subnormal below 2^-14 and 0 below 2^-25, while the sum keeps them
+// in fp32: behind one key with nearly all of the mass the others lost bits, and the output
+// is theirs where that key's value is small. So the reference then stands 2^6 below the
+// maximum: weights reach 2^14, times V's mantissa 2^15, and one of them is a normal
+// down to 2^-20 of the largest, and off by at most 2^-31 of it below.
+template <bool E4M3>
+constexpr float kHeadroom = E4M3 ? 6.f : 0.f;
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -278,6 +288,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   constexpr int D = TR::D, CH = TR::CH, NW = TR::NW, STAGES = TR::STAGES, TILE = TR::TILE;
   constexpr int ROWS = TR::ROWS, NR = TR::NR, MT = TR::MT;
   constexpr bool E4M3 = TR::E4M3;
+  constexpr float HEAD = kHeadroom<E4M3>;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* s_ring = smem;
   float* s_meta = reinterpret_cast<float*>(smem + TR::RING);  // [NW][STAGES][4]: K scale, V scale, page mapped
@@ -441,8 +452,8 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     for (int n = 0; n < MT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[r][n][e] = 0.f;
-  // m: reference of the row's exponents (a running max, raised only when it is
-  // exceeded by 2^8: sums and O are rescaled rarely); l: this lane's share of the
+  // m: reference of the row's exponents (a running max less the headroom, raised only when
+  // it is exceeded by 2^8: sums and O are rescaled rarely); l: this lane's share of the
   // sum. Over an 8-bit pool V's codes enter the MMA as they are and their scale
   // goes with P = p vs, so the reference is the max of x + log2(vs): P then stays
   // inside fp16 whatever the pages' scales are, p itself is fp32.
@@ -525,14 +536,14 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     bool raise = false;
 #pragma unroll
     for (int q = 0; q < 2 * NR; ++q)
-      raise = raise || fmaxf(sx[q >> 1][q & 1], sx[q >> 1][2 + (q & 1)]) + c2 > m[q] + 8.f;
+      raise = raise || fmaxf(sx[q >> 1][q & 1], sx[q >> 1][2 + (q & 1)]) + c2 > m[q] + (8.f + HEAD);
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int q = 0; q < 2 * NR; ++q) {
         float mx = fmaxf(sx[q >> 1][q & 1], sx[q >> 1][2 + (q & 1)]) + c2;
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        const float nm = fmaxf(m[q], mx);
+        const float nm = fmaxf(m[q], mx - HEAD);
         const float al = nm == -INFINITY ? 1.f : ex2(m[q] - nm);
         m[q] = nm;
         l[q] *= al;

@@ -18,7 +18,7 @@
 //    softmaxes in lockstep: 4500 clocks a tile pair.)
 //  * warps 8-11 and 12-15 are A's and B's softmax, a row per thread: maxima and
 //    sums in fp32; O is rescaled in tensor memory only when the reference is
-//    exceeded by 2^8.
+//    exceeded by 2^8 (2^14 over an 8-bit pool, where it starts 2^6 below the maximum).
 // 1024 queries of 32 heads over 32768 keys (8 K/V heads of 128): 551 us, 980 TFLOP/s, over a
 // bf16 pool, 642 us over an 8-bit one (its softmax reads the groups' scales and has 4
 // operand buffers instead of 5); without the ranges' ends on the SMs that 128 units leave
@@ -108,6 +108,7 @@ template <class TR, int MODS>
 __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const PagedAttnParams p) {
   constexpr int D = TR::D, BM = TR::BM, BN = TR::BN, STAGES = TR::STAGES, TILE = TR::TILE;
   constexpr bool E4M3 = TR::E4M3;
+  constexpr float HEAD = kHeadroom<E4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                 // [2][TILE]
@@ -575,8 +576,8 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         }
         float mx = fmaxf(fmax3(fmax3(mg[0], mg[1], mg[2]), mg[3], mg[4]), fmax3(mg[5], mg[6], mg[7]));
         if (!E4M3) mx *= f_all;
-        const bool raise = mx > m + 8.f;
-        const float m_use = raise ? mx : m;
+        const bool raise = mx > m + (8.f + HEAD);
+        const float m_use = raise ? mx - HEAD : m;
         // S_i complete implies that P V i - 1, issued before it, is
         if (__any_sync(0xffffffffu, raise) && i > 0) {
           const float al = raise ? ex2(m - m_use) : 1.f;

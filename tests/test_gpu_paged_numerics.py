@@ -1,0 +1,69 @@
+"""Attention over a paged pool where its roundings, ranges and masks can go wrong,
+as a whole (tests/paged_checks.py) and against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import sink_window_attention_b200 as swa
+from oracle import tokens
+from tests.paged_checks import norm_error
+from tests.test_gpu_tokens import Setup, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def expected(s, q, rope=None, **kw):
+    """The oracle's rows (and lse, and what bounds need) of a whole call."""
+    parts, at = [], 0
+    for b, n in enumerate(s.news):
+        x = f64(q[at:at + n])
+        if rope is not None:
+            x = tokens.rotate(x, np.arange(s.lens[b] - n, s.lens[b]), tokens.frequencies(rope.rot_dim), rope.layout)
+        (k, there), (v, _) = s.keys(b, "k"), s.keys(b, "v")
+        args = {**kw, "prefix": kw["prefix"][b]} if "prefix" in kw else kw
+        parts.append(tokens.attend(x, k, v, s.lens[b], exists=there, **args))
+        at += n
+    return [np.concatenate(p) for p in zip(*parts)]
+
+
+# ---------------------------------------------------------------------------
+# one key with nearly all of the mass
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("gap", [11.0, 13.5, 15.4])
+@pytest.mark.parametrize("sink", [0, 1390])
+def test_tail_behind_one_key(dtype, D, new, gap, sink):
+    """A pinned token with nearly all of the mass and a value of zero: the output is the
+    tail of some 1400 equal weights e^-gap below it. Each is rounded to bf16 (2^-8) or to
+    fp16: 2^-11, or half a step of the subnormals, 2^-31 of the largest weight. All are
+    equal, so their errors add up. The pinned key comes first, or last (the tail is then
+    made of fp16 normals, which shrink in fp32). So many units that no range is split:
+    the sink and its tail meet in one sum."""
+    B, H, n = (3 if new == 1 else 1), 128, 1400 + new
+    s = Setup([n] * B, [n] * B, H, D, dtype, 64)
+    k = torch.zeros((B, n, H, D), device="cuda")
+    v = 1 + torch.randn((B, n, H, D), generator=torch.Generator(device="cuda").manual_seed(D), device="cuda")
+    k[:, sink] = 8.0
+    v[:, sink] = 0.0
+    swa.paged_append(s.cache, s.batch(), k.view(-1, H, D).bfloat16(), v.view(-1, H, D).bfloat16())
+    s.take()
+    s.news = [new] * B
+    q = torch.ones((B * new, H, D), device="cuda").bfloat16()
+    lse = torch.empty((B * new, H), device="cuda")
+    got = f64(swa.paged_attention(q, s.cache, s.batch(), None, swa.Scores(softmax_scale=gap / (8.0 * D)), lse=lse))
+    want, total = np.zeros((B, new, H, D)), np.zeros((B, new, H))
+    w = np.full(n, np.exp(-gap))
+    w[sink] = 1.0
+    for b in range(B):
+        vals = s.keys(b, "v")[0].reshape(n, H * D)
+        for i in range(new):
+            seen = n - new + i + 1
+            total[b, i] = w[:seen].sum()
+            want[b, i] = (w[:seen] @ vals[:seen] / w[:seen].sum()).reshape(H, D)
+    want = want.reshape(got.shape)
+    rel = 2.0**-8 if dtype == "bf16" else max(2.0**-11, 2.0**-31 * np.exp(gap))
+    # and the output's rounding; the scale is held in fp32 (a score of gap is off by 2^-23 gap, ex2 by 2^-22)
+    assert norm_error(got, want) <= rel + 1.35 * 1.7e-3 + 4e-5
+    assert np.abs(f64(lse) - gap - np.log(total.reshape(lse.shape))).max() <= 4e-5
