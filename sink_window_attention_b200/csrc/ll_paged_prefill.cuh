@@ -179,12 +179,14 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
     regs_dec<TR::REGS_LOAD>();
     const int tid = threadIdx.x;
     // Lane g < 8 holds the place of keys [16 g, 16 g + 16) of a tile, which lie in
-    // one page: their page (-1: none) and their number in the pool's runs of 16 rows.
+    // one page: their page (-1: none, or no row sees one of them: neither their rows nor
+    // their scales are read then) and their number in the pool's runs of 16 rows.
     const int per_page = ps >> 4;
     auto page_for = [&](int i) -> int {
       if (lane >= 8 || i >= n) return -1;
       const int key = kr.tile(t_beg + i) * BN + lane * 16;
-      return key < s.len ? page_of(p.batch, b, key >> p.pool.page_shift, p.pool.n_pages) : -1;
+      const bool seen = key < kr.always || (key + 16 > kr.lo && key < kr.upper);
+      return seen ? page_of(p.batch, b, key >> p.pool.page_shift, p.pool.n_pages) : -1;
     };
     auto run_of = [&](int i, int page) -> int {
       return page < 0 ? -1 : (page * p.pool.H + hkv) * per_page + ((kr.tile(t_beg + i) * 8 + lane) & (per_page - 1));

@@ -6,7 +6,7 @@ import torch
 
 import sink_window_attention_b200 as swa
 from oracle import tokens
-from tests.paged_checks import norm_error
+from tests.paged_checks import norm_error, norm_limit
 from tests.test_gpu_tokens import Setup, f64
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +67,32 @@ def test_tail_behind_one_key(dtype, D, new, gap, sink):
     # and the output's rounding; the scale is held in fp32 (a score of gap is off by 2^-23 gap, ex2 by 2^-22)
     assert norm_error(got, want) <= rel + 1.35 * 1.7e-3 + 4e-5
     assert np.abs(f64(lse) - gap - np.log(total.reshape(lse.shape))).max() <= 4e-5
+
+
+# ---------------------------------------------------------------------------
+# scales
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("new", [1, 60, 140])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("mods", [dict(window=40, n_sink=3), dict(window=1100), dict(window=1100, n_sink=3),
+                                  dict(window=1033, n_sink=17, cap=4.0)])
+def test_scales_of_keys_that_no_row_sees(new, page, D, mods):
+    """Mapped pages before the window, or between the sinks and it, with NaN or
+    infinite scales (pages given back): what their places hold does not matter."""
+    s = Setup([1900, 1510], [new, new], 2, D, "fp8", page)
+    s.fill(3)
+    for b, n in enumerate(s.lens):
+        lo = n - new - mods["window"] + 1  # the first key that the window of the first row reaches
+        for pg in range(-(-mods.get("n_sink", 0) // page), lo // page):
+            at = int(s.table[b, pg])
+            for name in ("k_scale", "v_scale"):
+                getattr(s.cache, name)[at] = float("nan") if pg % 2 else float("inf")
+            s.cache.k[at] = 0x7F
+            s.cache.v[at] = 0x7F
+    q = torch.randn((2 * new, 4, D), device="cuda").bfloat16()
+    out = f64(swa.paged_attention(q, s.cache, s.batch(), None, swa.Scores(**{("soft_cap" if a == "cap" else a): x for a, x in mods.items()})))
+    for x in (s.pool.ks, s.pool.vs, s.pool.k, s.pool.v):
+        x[~np.isfinite(x)] = 0.0
+    want = expected(s, q, **mods)[0]
+    assert norm_error(out, want) <= norm_limit("fp8", 8 * new)
