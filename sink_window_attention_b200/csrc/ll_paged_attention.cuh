@@ -133,12 +133,20 @@ __device__ __forceinline__ float power_below(float a) {
   return __uint_as_float(static_cast<uint32_t>(e < 2 ? 2 : (e > 253 ? 253 : e)) << 23);
 }
 
-// floor(log2(s)) of a scale, kept within [-60, 60] (a zero scale: -60): only a
-// reference for exponents, which cancels. The bounds keep p in fp32.
-__device__ __forceinline__ float scale_exponent(float s) {
+// The exponent c of a V scale, kept within [-106, 126]. P enters the
+// MMA as 2^(x + c - m) and the sum takes 2^-c of it, so that P stays in fp16 whatever the
+// scales are. The sum is kept in units of 2^13 (8-bit pools), which centres it in fp32's
+// range: 2^20 weights of 2^14 at c = -106 come to 2^127 units, one of 2^6 at c = 119 (the
+// largest that bf16 values ask for) to 2^-126. Of values below some 2^-97 bits are lost.
+// A zero scale's codes are zeros and ask for no c: -40 leaves the other pages' P their bits,
+// and 80 binades to its own weights, which only the sum sees.
+__device__ __forceinline__ int scale_exponent(float s) {
   const int e = static_cast<int>(__float_as_uint(s) >> 23 & 255u) - 127;
-  return static_cast<float>(e < -60 ? -60 : (e > 60 ? 60 : e));
+  return e == -127 ? -40 : (e < -106 ? -106 : (e > 126 ? 126 : e));
 }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+template <bool E4M3>
+constexpr int kSumUnit = E4M3 ? 13 : 0;  // log2
 
 // The running reference of a row's exponents is raised where a score exceeds it by 2^8,
 // so a weight is at most 2^8. bf16 weights keep their 8 bits however small they are. fp16
@@ -288,7 +296,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   constexpr int D = TR::D, CH = TR::CH, NW = TR::NW, STAGES = TR::STAGES, TILE = TR::TILE;
   constexpr int ROWS = TR::ROWS, NR = TR::NR, MT = TR::MT;
   constexpr bool E4M3 = TR::E4M3;
-  constexpr float HEAD = kHeadroom<E4M3>;
+  constexpr float HEAD = kHeadroom<E4M3>, UNIT = 1.f / (1 << kSumUnit<E4M3>);
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* s_ring = smem;
   float* s_meta = reinterpret_cast<float*>(smem + TR::RING);  // [NW][STAGES][4]: K scale, V scale, page mapped
@@ -455,8 +463,8 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   // m: reference of the row's exponents (a running max less the headroom, raised only when
   // it is exceeded by 2^8: sums and O are rescaled rarely); l: this lane's share of the
   // sum. Over an 8-bit pool V's codes enter the MMA as they are and their scale
-  // goes with P = p vs, so the reference is the max of x + log2(vs): P then stays
-  // inside fp16 whatever the pages' scales are, p itself is fp32.
+  // goes with P = p vs, so the reference is the max of x + c, c the scale's exponent: P then
+  // stays inside fp16 whatever the pages' scales are.
   float m[2 * NR], l[2 * NR];
 #pragma unroll
   for (int q = 0; q < 2 * NR; ++q) m[q] = -INFINITY, l[q] = 0.f;
@@ -532,7 +540,10 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
           if (mt.z == 0.f || !row_sees(p.sc, kr, s.len, pos[2 * r + (e & 1)], j)) sx[r][e] = -INFINITY;
         }
     }
-    const float vs = E4M3 ? mt.y : 1.f, c2 = E4M3 ? scale_exponent(vs) : 0.f;
+    const int ce = E4M3 ? scale_exponent(mt.y) : 0;
+    const float c2 = static_cast<float>(ce);
+    const float inv_c = E4M3 ? power_of_two(-ce) : 1.f, mant = E4M3 ? mt.y * inv_c : 1.f;
+    const float share = inv_c * UNIT;  // of P, in the sum
     bool raise = false;
 #pragma unroll
     for (int q = 0; q < 2 * NR; ++q)
@@ -558,12 +569,13 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const float m0 = m[2 * r] == -INFINITY ? 0.f : m[2 * r], m1 = m[2 * r + 1] == -INFINITY ? 0.f : m[2 * r + 1];
-      const float e0 = ex2(sx[r][0] - m0), e1 = ex2(sx[r][1] - m1), e2 = ex2(sx[r][2] - m0), e3 = ex2(sx[r][3] - m1);
-      l[2 * r] += e0 + e2;
-      l[2 * r + 1] += e1 + e3;
+      const float f0 = c2 - m0, f1 = c2 - m1;
+      const float e0 = ex2(sx[r][0] + f0), e1 = ex2(sx[r][1] + f1), e2 = ex2(sx[r][2] + f0), e3 = ex2(sx[r][3] + f1);
+      l[2 * r] = fmaf(e0 + e2, share, l[2 * r]);
+      l[2 * r + 1] = fmaf(e1 + e3, share, l[2 * r + 1]);
       if constexpr (E4M3) {
-        pb[r][0] = transpose8x8(pack_f16(e0 * vs, e1 * vs));
-        pb[r][1] = transpose8x8(pack_f16(e2 * vs, e3 * vs));
+        pb[r][0] = transpose8x8(pack_f16(e0 * mant, e1 * mant));
+        pb[r][1] = transpose8x8(pack_f16(e2 * mant, e3 * mant));
       } else {
         pb[r][0] = transpose8x8(pack_bf16(e0, e1));
         pb[r][1] = transpose8x8(pack_bf16(e2, e3));
@@ -617,7 +629,10 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
   }
 
   // ---- join the block's warps
+  // (sums and O in the same units from here on)
   cp_async_wait<0>();
+#pragma unroll
+  for (int q = 0; q < 2 * NR; ++q) m[q] += static_cast<float>(kSumUnit<E4M3>);
 #pragma unroll
   for (int q = 0; q < 2 * NR; ++q)
 #pragma unroll
@@ -638,7 +653,7 @@ __global__ void __launch_bounds__(TR::THREADS, TR::BLOCKS) paged_decode_kernel(c
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * ROWS + row]);
-    const float f = m[q] == -INFINITY ? 0.f : ex2(m[q] - M);
+    const float f = m[q] == -INFINITY ? 0.f : ex2(m[q] - M) * UNIT;
     float* dst = s_o + (warp * ROWS + row) * D;
 #pragma unroll
     for (int n = 0; n < MT; ++n) {

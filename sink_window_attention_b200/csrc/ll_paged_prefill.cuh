@@ -68,7 +68,7 @@ struct PrefillTraits {
 struct KeyGroup {
   float ks;      // K scale
   float c;       // exponent of the V scale
-  float inv_c;   // 2^-c
+  float share;   // 2^-c in units of the sum
   float unused;
 };
 
@@ -108,7 +108,7 @@ template <class TR, int MODS>
 __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const PagedAttnParams p) {
   constexpr int D = TR::D, BM = TR::BM, BN = TR::BN, STAGES = TR::STAGES, TILE = TR::TILE;
   constexpr bool E4M3 = TR::E4M3;
-  constexpr float HEAD = kHeadroom<E4M3>;
+  constexpr float HEAD = kHeadroom<E4M3>, UNIT = 1.f / (1 << kSumUnit<E4M3>);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                 // [2][TILE]
@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         const unsigned mapped = __ballot_sync(0xffffffffu, pg >= 0);
         if (lane == 0) meta_mapped[i % TR::META] = static_cast<int>(mapped);
         if (E4M3 && lane < 8) {
-          const float c = scale_exponent(vs);
-          meta[(i % TR::META) * 8 + lane] = KeyGroup{ks, c, exp2f(-c), 0.f};
+          const int c = scale_exponent(vs);
+          meta[(i % TR::META) * 8 + lane] = KeyGroup{ks, static_cast<float>(c), power_of_two(-c) * UNIT, 0.f};
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&meta_full[i % TR::META]);
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         const int pg2 = page_for(i + 2);
         const float ks1 = scale_for(p.pool.k_scale, pg1), vs1 = scale_for(p.pool.v_scale, pg1);
         // V's scale without its exponent, for the 16 keys of lane g
-        const float mant = vs * exp2f(-scale_exponent(vs));
+        const float mant = vs * power_of_two(-scale_exponent(vs));
         const bool plain = __all_sync(0xffffffffu, lane >= 8 || mant == 1.f);
         const int run1 = run_of(i + 1, pg1);
 #pragma unroll 1
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
               sr[c][hf * 8 + e] = E4M3 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
             }
             const uint64_t sum = f2_add(part[0], part[1]);
-            if constexpr (E4M3) l2 = f2_fma(sum, f2_pack(kg[g].inv_c, kg[g].inv_c), l2);
+            if constexpr (E4M3) l2 = f2_fma(sum, f2_pack(kg[g].share, kg[g].share), l2);
             else l2 = f2_add(l2, sum);
           }
           tmem_store16(tS + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&sr[c][0]));
@@ -634,6 +634,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       // ---- epilogue
       if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[w], 0, s_abort));
       tc_fence_after();
+      m += static_cast<float>(kSumUnit<E4M3>);  // O below: times UNIT
       if (ok) {
         const size_t at = static_cast<size_t>(s.q0 + tok) * p.Hq + h;
         const bool none = m == -INFINITY;
@@ -652,7 +653,8 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
               uint32_t u[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                u[e] = none ? 0u : pack_bf16(__uint_as_float(o[q * 8 + 2 * e]) * inv, __uint_as_float(o[q * 8 + 2 * e + 1]) * inv);
+                u[e] = none ? 0u : pack_bf16(__uint_as_float(o[q * 8 + 2 * e]) * UNIT * inv,
+                                             __uint_as_float(o[q * 8 + 2 * e + 1]) * UNIT * inv);
               if (live) dst[q] = make_uint4(u[0], u[1], u[2], u[3]);
             }
             __syncwarp();
@@ -669,8 +671,9 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
             for (int q = 0; q < 8; ++q)
               if (live)
                 __stcg(dst + q, none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                     : make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                                                   __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3])));
+                                     : make_float4(__uint_as_float(o[4 * q]) * UNIT, __uint_as_float(o[4 * q + 1]) * UNIT,
+                                                   __uint_as_float(o[4 * q + 2]) * UNIT,
+                                                   __uint_as_float(o[4 * q + 3]) * UNIT));
             __syncwarp();
           }
           if (live) __stcg(p.part_ml + at * p.nsplit + split, make_float2(m, l));

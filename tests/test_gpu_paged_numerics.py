@@ -96,3 +96,21 @@ def test_scales_of_keys_that_no_row_sees(new, page, D, mods):
         x[~np.isfinite(x)] = 0.0
     want = expected(s, q, **mods)[0]
     assert norm_error(out, want) <= norm_limit("fp8", 8 * new)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 60, 140])
+@pytest.mark.parametrize("power", [-100, -70, 75, 110])
+def test_values_far_from_one(D, new, power):
+    """V of 2^-100 to 2^110 in every page: scales beyond what a fp16 product holds."""
+    s = Setup([300, 70], [300, 70], 2, D, "fp8", 32)
+    g = torch.Generator(device="cuda").manual_seed(power + 200)
+    k = torch.randn((370, 2, D), generator=g, device="cuda").bfloat16()
+    v = (torch.randn((370, 2, D), generator=g, device="cuda") * 2.0**power).bfloat16()
+    swa.paged_append(s.cache, s.batch(), k, v)
+    s.take()
+    s.news = [min(new, 300), min(new, 70)]
+    q = torch.randn((sum(s.news), 4, D), generator=g, device="cuda").bfloat16()
+    out = f64(swa.paged_attention(q, s.cache, s.batch()))
+    want = expected(s, q)[0]
+    assert norm_error(out * 2.0**-power, want * 2.0**-power) <= norm_limit("fp8", out.shape[0] * 4)
