@@ -532,13 +532,15 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
                                                   (p.sc.window == 0 || w_hi - key0 < p.sc.window)));
         if constexpr (MODS != 0) {
           const float away = MODS & kBiased ? offset_of(pos, key0) : 0.f;  // of key 0 of the tile
+          with_cap<MODS>(p.sc, [&](auto wide) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              sr[c][e] = __float_as_uint(score2<MODS>(p.sc, __uint_as_float(sr[c][e]),
-                                                      E4M3 ? fac * kg[2 * c + (e >> 4)].ks : fac, slope,
-                                                      away - static_cast<float>(c * 32 + e)));
+              for (int e = 0; e < 32; ++e)
+                sr[c][e] = __float_as_uint(score2<MODS, decltype(wide)::value>(
+                    p.sc, __uint_as_float(sr[c][e]), E4M3 ? fac * kg[2 * c + (e >> 4)].ks : fac, slope,
+                    away - static_cast<float>(c * 32 + e)));
+          });
         }
         if (!all_seen) {
           // 32 keys' visibility as bits, a test and a select per score (conditions joined

@@ -114,3 +114,24 @@ def test_values_far_from_one(D, new, power):
     out = f64(swa.paged_attention(q, s.cache, s.batch()))
     want = expected(s, q)[0]
     assert norm_error(out * 2.0**-power, want * 2.0**-power) <= norm_limit("fp8", out.shape[0] * 4)
+
+
+# ---------------------------------------------------------------------------
+# caps
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 140])
+@pytest.mark.parametrize("cap", [0.5, 30.0, 300.0, 1e4, 1e6, 1e30])
+def test_caps_far_above_the_scores(dtype, D, new, cap):
+    """cap * tanh(x / cap) keeps x's relative precision where the cap is far above it:
+    lse within 1e-5 (1 + |x|) of the definition's, whatever the cap."""
+    s = Setup([500], [500], 2, D, dtype, 32)
+    s.fill(7)
+    s.news = [new]
+    q = torch.randn((new, 4, D), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").bfloat16()
+    lse = torch.empty((new, 4), device="cuda")
+    out = f64(swa.paged_attention(q, s.cache, s.batch(), None, swa.Scores(soft_cap=cap), lse=lse))
+    want, ref, _, _ = expected(s, q, cap=cap)
+    assert np.abs(f64(lse) - ref).max() <= 3e-5 * (1 + np.abs(ref).max())
+    assert norm_error(out, want) <= norm_limit(dtype, 4 * new)
