@@ -7,7 +7,7 @@ import torch
 import sink_window_attention_b200 as swa
 from oracle import tokens
 from tests.paged_checks import norm_error, norm_limit
-from tests.test_gpu_tokens import Setup, f64
+from tests.test_gpu_tokens import MODS, SHAPES, Setup, f64, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,70 @@ def test_caps_far_above_the_scores(dtype, D, new, cap):
     want, ref, _, _ = expected(s, q, cap=cap)
     assert np.abs(f64(lse) - ref).max() <= 3e-5 * (1 + np.abs(ref).max())
     assert norm_error(out, want) <= norm_limit(dtype, 4 * new)
+
+
+# ---------------------------------------------------------------------------
+# outputs as a whole
+# ---------------------------------------------------------------------------
+LONG = [  # few rows: pieces joined in a cluster, and through the workspace
+    ([1500], [1], 2, 4, 64, 16),
+    ([2000, 1800, 40], [2, 1, 1], 4, 2, 128, 64),
+    ([20011], [1], 2, 8, 128, 64),
+    ([9000, 33000], [1, 3], 1, 5, 64, 128),
+]
+
+
+def growing(s, seed):
+    """Keys whose size grows along a sequence, so that pieces of it weigh differently;
+    values of mean zero."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = sum(s.lens)
+    at = torch.cat([torch.linspace(0.4, 1.2, m) for m in s.lens]).cuda()[:, None, None]
+    k = (torch.randn((n, s.H, s.D), generator=g, device="cuda") * at).bfloat16()
+    v = torch.randn((n, s.H, s.D), generator=g, device="cuda").bfloat16()
+    swa.paged_append(s.cache, s.batch(news=s.lens), k, v)
+    s.take()
+
+
+@pytest.mark.parametrize("lens,news,H,group,D,page", SHAPES + LONG)
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("mod", list(MODS))
+def test_norm_of_the_error(lens, news, H, group, D, page, dtype, mod):
+    s = Setup(lens, news, H, D, dtype, page, seed=3, garbage=True)
+    growing(s, 17)
+    kw = dict(MODS[mod])
+    Hq = H * group
+    if kw.pop("bias", False):
+        kw["slopes"] = [float(2.0 ** (-1 - h)) for h in range(Hq)]
+    if kw.pop("prefix", False):
+        kw["prefix"] = [n // 2 + 1 if b % 2 == 0 else 0 for b, n in enumerate(lens)]
+    rope = swa.TokenRope(64) if mod == "plain" else swa.TokenRope(32, layout="interleaved") if mod == "sink" else None
+    g = torch.Generator(device="cuda").manual_seed(23)
+    q = torch.randn((sum(news), Hq, D), generator=g, device="cuda").bfloat16()
+    sc = swa.Scores(softmax_scale=kw.get("scale", 0.0), window=kw.get("window", 0), n_sink=kw.get("n_sink", 0),
+                    soft_cap=kw.get("cap", 0.0), slopes=kw.get("slopes"),
+                    prefix_len=i32(kw["prefix"]) if "prefix" in kw else None)
+    out = f64(swa.paged_attention(q, s.cache, s.batch(), rope, sc))
+    want = expected(s, q, rope, **kw)[0]
+    one_term = rope is not None and max(news) * group > 8
+    assert norm_error(out, want) <= norm_limit(dtype, sum(news) * Hq, 1.2 if one_term else 0.0)
+    assert swa.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 140])
+def test_norm_of_the_error_where_pages_are_powers_of_two_apart(dtype, D, new):
+    """Values 2^-20 to 2^20 by page, and keys that grow: each row's output is that of the
+    few pages that count for it."""
+    s = Setup([1700], [1700], 2, D, dtype, 16, garbage=True)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    k = torch.randn((1700, 2, D), generator=g, device="cuda") * torch.linspace(0.1, 2, 1700, device="cuda")[:, None, None]
+    v = torch.randn((1700, 2, D), generator=g, device="cuda")
+    v = v * torch.exp2(((torch.arange(1700, device="cuda") // 16) * 7 % 41 - 20).float())[:, None, None]
+    swa.paged_append(s.cache, s.batch(), k.bfloat16(), v.bfloat16())
+    s.take()
+    s.news = [new]
+    q = torch.randn((new, 4, D), generator=g, device="cuda").bfloat16()
+    out = f64(swa.paged_attention(q, s.cache, s.batch()))
+    assert norm_error(out, expected(s, q)[0]) <= norm_limit(dtype, 4 * new)
