@@ -450,7 +450,7 @@ def selftest_bounded_waits(stream=None) -> int:
 # and attention of a ragged batch of sequences over it.
 # ---------------------------------------------------------------------------
 # These calls are made once per layer and token, so the marshalling is kept short:
-# one look at the current device, descriptors rebuilt only when a tensor changed.
+# one look at the current device, descriptors kept until something they were made of changes.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -465,6 +465,26 @@ def _on(t: torch.Tensor, device: int) -> int:
     if t.get_device() != device or not t.is_contiguous():
         return _ptr(t)
     return t.data_ptr()
+
+
+def _fits(t: Optional[torch.Tensor], shape, dtype: torch.dtype, what: str) -> None:
+    if t is None:
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}, got None")
+    _expect(t, shape, dtype, what)
+
+
+class _Described:
+    """Keeps the descriptor of its fields. Setting one drops it; what else can change is a
+    tensor in place (its address, size or order), which each call looks at."""
+    _kept = (None, None)  # what the descriptor's tensors were, and the descriptor, replaced together
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_kept", (None, None))
+
+    def _keep(self, now, c):
+        object.__setattr__(self, "_kept", (now, c))
+        return c
 
 
 class TokenRope:
@@ -491,36 +511,55 @@ class TokenRope:
         return self._c
 
 
-class PagedKVCache:
+_POOL_TYPES = {"bf16": (LL_BF16, torch.bfloat16), "fp8": (LL_FP8_E4M3, torch.uint8)}
+
+
+class PagedKVCache(_Described):
     """One layer's pool of pages in device memory (mirrors ll_paged_cache):
     k, v [n_pages, H, page_size, D]; an "fp8" pool has k_scale, v_scale [n_pages, H]."""
 
     def __init__(self, n_pages: int, page_size: int, H: int, D: int, dtype: str = "bf16", device: str = "cuda"):
         self.n_pages, self.page_size, self.H, self.D, self.dtype = n_pages, page_size, H, D, dtype
+        code, tdt = _POOL_TYPES[dtype]
         shape = (n_pages, H, page_size, D)
-        tdt = {"bf16": torch.bfloat16, "fp8": torch.uint8}[dtype]
         self.k = torch.zeros(shape, dtype=tdt, device=device)
         self.v = torch.zeros(shape, dtype=tdt, device=device)
         self.k_scale = self.v_scale = None
         if dtype == "fp8":
             self.k_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
             self.v_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
-        self.code = LL_FP8_E4M3 if dtype == "fp8" else LL_BF16
-        self._kept = ((), None)  # addresses and descriptor, replaced together
+        self.code = code
+
+    def _now(self, device):
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        if ks is None:
+            return (device, k.data_ptr(), k.numel(), k.is_contiguous(), v.data_ptr(), v.numel(), v.is_contiguous())
+        return (device, k.data_ptr(), k.numel(), k.is_contiguous(), v.data_ptr(), v.numel(), v.is_contiguous(),
+                ks.data_ptr(), ks.numel(), ks.is_contiguous(), vs.data_ptr(), vs.numel(), vs.is_contiguous())
 
     def to_c(self, device: Optional[int] = None) -> PagedCacheC:
-        """The descriptor; with a device, its tensors are checked to be there."""
-        tensors = (self.k, self.v) if self.k_scale is None else (self.k, self.v, self.k_scale, self.v_scale)
-        at = tuple([t.data_ptr() if device is None else _on(t, device) for t in tensors])
+        """The descriptor, of tensors that fit the pool's sizes and type; with a device,
+        they are checked to be there."""
         kept, c = self._kept
-        if at != kept:
-            c = PagedCacheC(*(at if len(at) == 4 else at + (None, None)), self.code, self.n_pages, self.page_size,
-                            self.H, self.D)
-            self._kept = (at, c)
-        return c
+        if c is not None and kept == self._now(device):
+            return c
+        code, tdt = _POOL_TYPES[self.dtype]
+        shape = (self.n_pages, self.H, self.page_size, self.D)
+        for t, what in ((self.k, "k"), (self.v, "v")):  # codes may be named by their own type too
+            codes = self.dtype == "fp8" and t is not None and t.dtype == torch.float8_e4m3fn
+            _fits(t, shape, torch.float8_e4m3fn if codes else tdt, what)
+        for t, what in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale")):
+            if self.dtype == "fp8":
+                _fits(t, shape[:2], torch.float32, what)
+            elif t is not None:
+                raise ValueError(f"{what} must be None in a {self.dtype} pool")
+        at = [t if t is None else (t.data_ptr() if device is None else _on(t, device))
+              for t in (self.k, self.v, self.k_scale, self.v_scale)]
+        return self._keep(self._now(device), PagedCacheC(*at, code, self.n_pages, self.page_size, self.H,
+                                                        self.D))
 
 
-class TokenBatch:
+class TokenBatch(_Described):
     """Which tokens of which sequences a call works on (mirrors ll_token_batch).
 
     q_start [B+1], kv_len [B], page_table [B, max_pages]: contiguous int32 CUDA
@@ -533,21 +572,29 @@ class TokenBatch:
         if page_table.dim() != 2:
             raise ValueError(f"page_table must be [B, max_pages], got shape {tuple(page_table.shape)}")
         B, max_pages = page_table.shape
-        _expect(page_table, (B, max_pages), torch.int32, "page_table")
-        _expect(q_start, (B + 1,), torch.int32, "q_start")
-        _expect(kv_len, (B,), torch.int32, "kv_len")
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
         self.B, self.max_pages, self.max_q, self.max_kv = B, max_pages, int(max_q), int(max_kv)
-        self._kept = ((), None)  # fields and descriptor, replaced together
+        self._check()
+
+    def _check(self) -> None:
+        _fits(self.page_table, (self.B, self.max_pages), torch.int32, "page_table")
+        _fits(self.q_start, (self.B + 1,), torch.int32, "q_start")
+        _fits(self.kv_len, (self.B,), torch.int32, "kv_len")
+
+    def _now(self, total_q, device):
+        q, n, p = self.q_start, self.kv_len, self.page_table
+        return (total_q, device, q.data_ptr(), q.numel(), q.is_contiguous(), n.data_ptr(), n.numel(),
+                n.is_contiguous(), p.data_ptr(), p.numel(), p.is_contiguous())
 
     def to_c(self, total_q: int, device: int) -> TokenBatchC:
-        key = (_on(self.q_start, device), _on(self.kv_len, device), _on(self.page_table, device), self.B,
-               self.max_pages, total_q, self.max_q, self.max_kv)
         kept, c = self._kept
-        if key != kept:  # a new structure, not a changed one: another thread may be in a call with the old
-            c = TokenBatchC(*key)
-            self._kept = (key, c)
-        return c
+        if c is not None and kept == self._now(total_q, device):
+            return c
+        self._check()
+        # a new structure, not a changed one: another thread may be in a call with the old
+        return self._keep(self._now(total_q, device),
+                          TokenBatchC(_on(self.q_start, device), _on(self.kv_len, device), _on(self.page_table, device),
+                                      self.B, self.max_pages, total_q, self.max_q, self.max_kv))
 
 
 class Scores:
