@@ -659,10 +659,41 @@ def _workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
         return like.new_empty((nbytes,), dtype=torch.uint8)
 
 
+def _as_rows(g: torch.Tensor) -> torch.Tensor:
+    """g, copied where it is no token tensor (an expanded, permuted or unaligned gradient)."""
+    T, H, D = g.shape
+    sr, sh, sd = g.stride()
+    if sd == 1 and sh == D and sr >= H * D and sr % 8 == 0 and g.data_ptr() % 16 == 0:
+        return g
+    return g.clone(memory_format=torch.contiguous_format)
+
+
+class _TokenRotation(torch.autograd.Function):
+    """The rotation is linear: its gradient is the transposed one's."""
+
+    @staticmethod
+    def forward(ctx, x, positions, rope, transpose):
+        ctx.save_for_backward(positions)
+        ctx.rope, ctx.transpose = rope, transpose
+        return token_rope_apply(x.detach(), positions, rope, transpose)
+
+    @staticmethod
+    def backward(ctx, g):
+        positions, = ctx.saved_tensors
+        return token_rope_apply(_as_rows(g), positions, ctx.rope, not ctx.transpose), None, None, None
+
+
 def token_rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: TokenRope, transpose: bool = False,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotate x [T, H, D] (bf16 or f32) at its tokens' positions (int32 [T]);
-    transpose=True applies the transposed rotation: the gradient. out may be x."""
+    transpose=True applies the transposed rotation: the gradient, which autograd
+    takes by itself where x requires grad. out may be x (not where autograd
+    tracks either)."""
+    if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
+        if out is not None:
+            raise ValueError("out cannot be given where x or out requires grad")
+        with torch.cuda.stream(stream):  # None: the current stream
+            return _TokenRotation.apply(x, positions, rope, bool(transpose))
     dev = _device(x)
     xp, xs = _rows(x, "x", dev)
     T, H, D = x.shape

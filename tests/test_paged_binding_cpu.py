@@ -144,3 +144,14 @@ def test_a_batch_whose_sizes_change():
     t.max_q = 7
     c = t.to_c(6, -1)
     assert (c.max_pages, c.max_q, c.page_table) == (50, 7, t.page_table.data_ptr())
+
+
+def test_a_rotation_in_place_of_what_autograd_tracks():
+    x = torch.zeros(2, 2, 64)
+    pos = torch.zeros(2, dtype=torch.int32)
+    for a, out in ((x.clone().requires_grad_(), x), (x, x.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="requires grad"):
+            swa.token_rope_apply(a, pos, swa.TokenRope(64), out=out)
+    y = x.clone().requires_grad_()
+    with pytest.raises(ValueError, match="requires grad"):
+        swa.token_rope_apply(y, pos, swa.TokenRope(64), out=y)
