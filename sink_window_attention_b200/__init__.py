@@ -714,10 +714,18 @@ def token_rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: TokenRope, 
     return out
 
 
+def _no_gradients(call: str) -> None:
+    if torch.is_grad_enabled():
+        raise ValueError(f"{call} has no gradients: call it under torch.no_grad(), or detach its inputs")
+
+
 def paged_append(cache: PagedKVCache, batch: TokenBatch, k: torch.Tensor, v: torch.Tensor,
                  rope: Optional[TokenRope] = None, stream=None) -> None:
     """Write the batch's new tokens, k and v [total_q, H, D] bf16, into their
-    pages, K rotated at its positions (ll_paged_append). Rows may be strided."""
+    pages, K rotated at its positions (ll_paged_append). Rows may be strided. There are
+    no gradients: inputs that require them are refused where grad is enabled."""
+    if k.requires_grad or v.requires_grad:
+        _no_gradients("paged_append")
     dev = _device(k)
     kp, ks = _rows(k, "k", dev, cache.H, cache.D)
     vp, vs = _rows(v, "v", dev, cache.H, cache.D)
@@ -742,7 +750,10 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: TokenBatch, rop
     """Attention of the batch's rows q [total_q, Hq, D] (bf16, rows may be
     strided; rotated here when rope is given) over the pool, which already holds
     their keys and values (ll_paged_attention). Rows of no sequence are not
-    written: they keep what `out` held."""
+    written: they keep what `out` held. There are no gradients: inputs that require them
+    are refused where grad is enabled."""
+    if q.requires_grad or (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad):
+        _no_gradients("paged_attention")
     dev = _device(q)
     qp, qs = _rows(q, "q", dev, None, cache.D)
     T, Hq, D = q.shape

@@ -155,3 +155,16 @@ def test_a_rotation_in_place_of_what_autograd_tracks():
     y = x.clone().requires_grad_()
     with pytest.raises(ValueError, match="requires grad"):
         swa.token_rope_apply(y, pos, swa.TokenRope(64), out=y)
+
+
+def test_inputs_that_require_grad_are_refused():
+    """The append and the attention have no gradients: under grad mode they say so."""
+    c, t = pool("bf16"), batch()
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    y = x.clone().requires_grad_()
+    for call in (lambda: swa.paged_append(c, t, y, x), lambda: swa.paged_append(c, t, x, y),
+                 lambda: swa.paged_attention(y, c, t), lambda: swa.paged_attention(x, c, t, out=y)):
+        with pytest.raises(ValueError, match="no_grad"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # the next check: host tensors
+            call()
