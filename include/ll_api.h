@@ -526,8 +526,8 @@ typedef struct ll_score_desc {
  * Keys that no query of a tile of rows sees are not read, so what their places
  * hold does not matter; a NaN or infinity in a key or value that some query of
  * the call sees may spoil the call's other rows of that sequence too.
- * Over a BF16 pool the softmax weights are rounded to bf16, and the rotated q to bf16
- * (calls of more than a few rows) or to two bf16 terms;
+ * Over a BF16 pool the softmax weights are rounded to bf16, and the rotated q to two bf16
+ * terms (one where D is 128 and the call has more than a few rows);
  * over an FP8 pool codes are used exactly, q and weights are rounded to fp16
  * under a power-of-two scale (weights below 2^-20 of a row's largest to steps of 2^-30 of it). Sums, maxima and outputs before the last rounding
  * are fp32.

@@ -46,9 +46,13 @@ struct PrefillTraits {
   static constexpr int CTRL = 2048;
   // 8-bit pools: a tile's codes of K and V on their way to fp16
   static constexpr int RAW = E4M3 ? 2 * BN * D : 0;
-  static constexpr int STAGES = (232448 - CTRL - 1024 - RAW - 2 * TILE) / TILE < 8
-                                    ? (232448 - CTRL - 1024 - RAW - 2 * TILE) / TILE : 8;
-  static constexpr int SMEM = CTRL + 1024 + (2 + STAGES) * TILE + RAW;
+  // Terms of a rotated q: two bf16 ones where their tiles fit beside the buffers that the
+  // issue order needs. At D = 128 they do not (two more tiles of 32 KB leave 3 of 5
+  // buffers), and fp16 (8-bit pools) has three bits more in one.
+  static constexpr int QS = !E4M3 && D == 64 ? 2 : 1;
+  static constexpr int FREE = (232448 - CTRL - 1024 - RAW) / TILE - 2 * QS;
+  static constexpr int STAGES = FREE < 8 ? FREE : 8;
+  static constexpr int SMEM = CTRL + 1024 + (2 * QS + STAGES) * TILE + RAW;
   // Slots of per-tile page data. Slot i is written again with buffer K_(i+META),
   // which can only be filled once V_i was consumed (2 META - STAGES >= 1), that is
   // after both softmax warpgroups handed over P_i and so have read slot i.
@@ -72,8 +76,14 @@ struct KeyGroup {
   float unused;
 };
 
+// What two values lose when they are rounded to bf16, as bf16.
+__device__ __forceinline__ uint32_t pack_bf16_rest(float a, float b) {
+  const float2 f = __bfloat1622float2(__floats2bfloat162_rn(a, b));
+  return pack_bf16(a - f.x, b - f.y);
+}
+
 // Like turn_of, with the hardware's sine and cosine of at most an eighth of a
-// turn (within 2^-21): for queries, which are rounded to 16 bits right after.
+// turn (within 2^-21): for queries, which keep 11 to 16 bits right after.
 __device__ __forceinline__ float2 turn_fast(const TokenRope& r, int pos, int i) {
   const uint32_t t = turned(pos, r.turns[i]);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
@@ -111,8 +121,8 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
   constexpr float HEAD = kHeadroom<E4M3>, UNIT = 1.f / (1 << kSumUnit<E4M3>);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;                 // [2][TILE]
-  uint8_t* sKV = smem + 2 * TILE;     // [STAGES][TILE]
+  uint8_t* sQ = smem;                      // [2][QS][TILE]
+  uint8_t* sKV = smem + 2 * TR::QS * TILE;  // [STAGES][TILE]
   uint8_t* sRaw = sKV + STAGES * TILE;  // [2][BN / RPS][128] chunks
   uint8_t* ctrl = sRaw + TR::RAW;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);  // [STAGES]
@@ -378,13 +388,19 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
         if (leader) mma_commit(bar);
       };
       auto issue_s = [&](int w, int st) {
-        const DescWords q{q_lo + w * (TILE >> 4), hi}, kd{k_lo + st * (TILE >> 4), hi};
+        const DescWords q{q_lo + w * (TR::QS * TILE >> 4), hi}, kd{k_lo + st * (TILE >> 4), hi};
         const uint32_t d = tbase + TR::S_COL + w * BN;
         if (leader) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = (k >> 2) * (BM * 128) + (k & 3) * 32;
             mma_bf16_ss(d, desc_at(q, off), desc_at(kd, off), idS, k > 0);
+          }
+          if constexpr (TR::QS == 2) {  // the second terms of what is rotated
+            const DescWords q2{q.lo + (TILE >> 4), hi};
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              if (k * 16 < p.rope.rot) mma_bf16_ss(d, desc_at(q2, k * 32), desc_at(kd, k * 32), idS, true);
           }
           mma_commit(&s_full[w]);
         }
@@ -450,7 +466,7 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
       float qf = 1.f;
       {
         const __nv_bfloat16* src = p.q + static_cast<long long>(s.q0 + (live ? tok : 0)) * p.q_stride + h * D;
-        uint8_t* dst = sQ + w * TILE;
+        uint8_t* dst = sQ + w * (TR::QS * TILE);
         uint4 raw[D / 8];  // the whole row in flight at once
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
@@ -481,6 +497,16 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
 #pragma unroll
             for (int e = 0; e < 8; ++e) cs[e] = turn_fast(p.rope, pos, c * 8 + e);
             rotate_item(p.rope, x, y, cs, 1);
+            if constexpr (TR::QS == 2) {
+              uint32_t v[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                v[e] = pack_bf16_rest(x[2 * e], x[2 * e + 1]);
+                v[4 + e] = pack_bf16_rest(y[2 * e], y[2 * e + 1]);
+              }
+              *reinterpret_cast<uint4*>(dst + TILE + sw128_offset(row, lo)) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(dst + TILE + sw128_offset(row, hi)) = make_uint4(v[4], v[5], v[6], v[7]);
+            }
           }
           uint32_t u[8];
 #pragma unroll

@@ -202,3 +202,18 @@ def test_norm_of_the_error_where_pages_are_powers_of_two_apart(dtype, D, new):
     q = torch.randn((new, 4, D), generator=g, device="cuda").bfloat16()
     out = f64(swa.paged_attention(q, s.cache, s.batch()))
     assert norm_error(out, expected(s, q)[0]) <= norm_limit(dtype, 4 * new)
+
+
+@pytest.mark.parametrize("rot,layout", [(64, "half"), (32, "interleaved"), (16, "half")])
+@pytest.mark.parametrize("H,group,new", [(2, 4, 140), (1, 1, 300)])
+def test_rotated_queries_of_large_scores(rot, layout, H, group, new):
+    """Heads of 64 over a bf16 pool, scores of standard deviation 3: a rotated q in one
+    bf16 term is off by 3.3 R of the output, in two by 1.4 R, whichever kernel is taken."""
+    s = Setup([1500 + new], [1500 + new], H, 64, "bf16", 16, garbage=True)
+    s.fill(9)
+    s.news = [new]
+    rope = swa.TokenRope(rot, layout=layout)
+    q = 3 * torch.randn((new, H * group, 64), generator=torch.Generator(device="cuda").manual_seed(8), device="cuda")
+    q = q.bfloat16()
+    out = f64(swa.paged_attention(q, s.cache, s.batch(), rope))
+    assert norm_error(out, expected(s, q, rope)[0]) <= norm_limit("bf16", new * H * group)
