@@ -689,7 +689,7 @@ def token_rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: TokenRope, 
     transpose=True applies the transposed rotation: the gradient, which autograd
     takes by itself where x requires grad. out may be x (not where autograd
     tracks either)."""
-    if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
+    if (x.requires_grad or (out is not None and out.requires_grad)) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot be given where x or out requires grad")
         with torch.cuda.stream(stream):  # None: the current stream
