@@ -78,7 +78,7 @@ __device__ __forceinline__ KeyRange key_range(const ScoreParams& sc, int b, cons
 }
 
 __device__ __forceinline__ bool row_sees(const ScoreParams& sc, const KeyRange& r, int len, int p, int j) {
-  // bitwise: short-circuits would be branches
+  // bitwise, so that nothing has to be skipped
   const bool near = static_cast<unsigned>(p) - static_cast<unsigned>(j) < static_cast<unsigned>(sc.window);
   return (j < r.prefix) | ((j <= p) & (j < len) & ((sc.window == 0) | near | (j < sc.n_sink)));
 }
