@@ -46,9 +46,12 @@ struct PrefillTraits {
   static constexpr int CTRL = 2048;
   // 8-bit pools: a tile's codes of K and V on their way to fp16
   static constexpr int RAW = E4M3 ? 2 * BN * D : 0;
-  // Terms of a rotated q: two bf16 ones where their tiles fit beside the buffers that the
-  // issue order needs. At D = 128 they do not (two more tiles of 32 KB leave 3 of 5
-  // buffers), and fp16 (8-bit pools) has three bits more in one.
+  // Terms of a rotated q. One bf16 term is off by 2^-9 of each element, which no V averages
+  // out (output error 3.6e-3 of its norm, two terms 2.3e-3). At D = 64 two more tiles of
+  // 16 KB fit beside the buffers and the second product hides (ragged prompts of 32 heads:
+  // 218 us rotated, 202 not). At D = 128 they would leave 3 of 5 buffers, and the products
+  // would be most of a tile's time: 2 to 3 thousand rows 249 -> 285 us, a chunk of 1024 over
+  // 32768 582 -> 711, so there one term stays. fp16 (8-bit pools) has three bits more in one.
   static constexpr int QS = !E4M3 && D == 64 ? 2 : 1;
   static constexpr int FREE = (232448 - CTRL - 1024 - RAW) / TILE - 2 * QS;
   static constexpr int STAGES = FREE < 8 ? FREE : 8;
@@ -434,6 +437,8 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
             issue_pv(w, h, v_st, i == 0 && h == 0, !more && h == 1);
           }
           if (!ok) break;
+          // V_i's last use: before the next S, whose products would hold its buffer longer
+          if (w == tiles - 1) commit(&empty[v_st]);
           if (!more) continue;
           if (w == 0) {
             if (!(ok = wait(&full[st], round & 1))) break;
@@ -442,7 +447,6 @@ __global__ void __launch_bounds__(TR::THREADS, 1) paged_prefill_kernel(const Pag
           issue_s(w, st);
         }
         if (!ok) break;
-        commit(&empty[v_st]);
         if (more) {
           commit(&empty[st]);
           if (++st == STAGES) st = 0, ++round;
