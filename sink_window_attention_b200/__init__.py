@@ -541,7 +541,7 @@ class PagedKVCache(_Described):
         """The descriptor, of tensors that fit the pool's sizes and type; with a device,
         they are checked to be there."""
         kept, c = self._kept
-        if c is not None and kept == self._now(device):
+        if c is not None and kept == self._now(kept[0] if device is None else device):
             return c
         code, tdt = _POOL_TYPES[self.dtype]
         shape = (self.n_pages, self.H, self.page_size, self.D)

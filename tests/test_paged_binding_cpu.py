@@ -23,6 +23,15 @@ def test_a_pool_that_grows():
     assert fields(c.to_c()) == (9, 16, 2, 64, swa.LL_BF16, c.k.data_ptr(), c.v.data_ptr(), None, None)
 
 
+def test_a_look_without_a_device_keeps_the_descriptor():
+    """(as the workspace's size asks for it between two calls)"""
+    c = pool()
+    a = c.to_c(-1)
+    assert c.to_c() is a and c.to_c(-1) is a
+    with pytest.raises(ValueError, match="CUDA"):
+        c.to_c(0)
+
+
 def test_sizes_are_part_of_what_is_kept():
     """Sizes that change under the same tensors: another descriptor, or a refusal."""
     c = pool("bf16")
