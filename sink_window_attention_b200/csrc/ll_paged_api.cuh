@@ -119,14 +119,18 @@ ll_status allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
 // How a call's rows and keys are divided among blocks. A function of the host's
 // bounds alone, so the workspace size is known before the call.
 // Rows of a sequence and K/V head up to which the decode kernel is taken. 8 sequences of
-// 2000-8000 keys, 8-bit: 48 rows 64 us (tiles of 128 rows: 89), 64 rows 81 (92), 96 rows
-// 109 (94); bf16: 48 rows 70 (81), 64 rows 89 (83).
+// 2000 to 8000 keys, 8 K/V heads of 128, decode (tiles of 128 rows): 8-bit 48 rows 68 us
+// (80), 64 rows 82 (82), 96 rows 120 (84); bf16 32 rows 60 (70), 48 rows 80 (70), 64 rows
+// 100 (72); heads of 64, bf16 48 rows 51 (64), 64 rows 62 (65). From 33 to 48 rows over a
+// bf16 pool of heads of 128 the tiles would be faster, but they keep a rotated q in one term.
 constexpr int kDecodeRows = 48;
 // Over short ranges, which stay in L2, it is taken for more rows where its waves of
 // blocks (6 us to start and end one, 0.08 us per 16 keys of 128 elements) take less than
-// the tile kernel's (10 us, 2.4 us per 128 keys). 1000 keys, decode (tiles): one sequence,
-// 8 K/V heads of 128, 512 rows 21 us (27), 1024 rows 38 (34); six, 256 rows 23 (35), 512
-// rows 40 (33); six, 12 heads of 64, 256 rows 25 (36), 512 rows 30 (26).
+// the tile kernel's (10 us, 2.4 us per 128 keys). 1000 keys, bf16, decode (tiles): one
+// sequence, 8 K/V heads of 128, 256 rows 19 us (21), 512 rows 23 (27), 1024 rows 41 (35); six
+// of 512 rows 115 (29), 12 heads of 64 79 (25). The estimate leaves out what blocks that read the
+// same keys cost L2, and what a split costs the tile kernel: with six full sequences of 256
+// rows it takes decode, 62 us (45), heads of 64 49 (49).
 constexpr long long kShortRange = 1024;
 
 // Blocks of the decode kernel that an SM holds.

@@ -114,8 +114,8 @@ __device__ __forceinline__ float offset_of(int p, int j) {
 // tanh(y) = 1 - 2 / (1 + e^2y): within about 2e-7 absolute, which the cap scales (to some
 // 1e-5 of a score at a cap of 64; the hardware's own tanh is off by 5e-4). Near 0 that is
 // no relative precision, so where the cap is WIDE the series y - y^3/3 + 2 y^5/15 -
-// 17 y^7/315 is taken below 1/4, whose rest is 1e-7 of y. Taken for every cap it made
-// capped tiles of 128 rows 148 -> 162 us (2619 tokens of 16 heads of 128, bf16 pool).
+// 17 y^7/315 is taken below 1/4, whose rest is 1e-7 of y. Taken for every cap it would make
+// capped tiles of 128 rows 132 -> 156 us (2619 tokens of 16 heads of 128, bf16 pool).
 constexpr float kWideCap = 64.f;
 
 template <bool WIDE>
@@ -249,10 +249,12 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t& lo, uint32_t
 //    the lane reads the V rows of keys 2t, 2t+1, 2t+8, 2t+9 at chunk g (+ 8), and
 //    byte permutes pair two keys at the same d.
 // One query per sequence, 8 K/V heads of 128: 4 sequences of up to 131000 keys (64 query
-// heads, 8-bit pool, 701 MB) 127 us, 5.5 TB/s, 84 % of a copy's rate; 48 of 2000 to 8000
-// (472 MB) 94 us, 5.0 TB/s; bf16 pool, the same 48 (945 MB) 153 us, 6.2 TB/s. With query
+// heads, 8-bit pool, 701 MB) 128 us, 5.5 TB/s, 83 % of a copy's rate; 48 of 2000 to 8000
+// (472 MB) 95 us, 5.0 TB/s; bf16 pool, the same 48 (945 MB) 153 us, 6.2 TB/s. With query
 // rows as the MMA's 16 rows the 8-bit batch took 110 us, with a conversion per E4M3 pair
-// that unpacked its operand 178 us.
+// that unpacked its operand 178 us. P in bf16 over a bf16 pool is what the matrix
+// instruction takes beside V; its rounding is averaged over the keys (2.3e-3 of the
+// output's norm in all, the output's own rounding 1.7e-3).
 // ---------------------------------------------------------------------------
 template <int D_, bool E4M3_, int ROWS_>
 struct DecodeTraits {

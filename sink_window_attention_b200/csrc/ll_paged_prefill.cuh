@@ -15,16 +15,18 @@
 //    the two from wanting the exponential unit at the same time. P is handed over in
 //    halves, so P V begins under the second half's exponentials. (S in halves of 64
 //    keys, double-buffered, so that no softmax ever waited for its own MMAs, ran both
-//    softmaxes in lockstep: 4500 clocks a tile pair.)
+//    softmaxes in lockstep and was slower: 599 us against 565 then.)
 //  * warps 8-11 and 12-15 are A's and B's softmax, a row per thread: maxima and
 //    sums in fp32; O is rescaled in tensor memory only when the reference is
 //    exceeded by 2^8 (2^14 over an 8-bit pool, where it starts 2^6 below the maximum).
-// 1024 queries of 32 heads over 32768 keys (8 K/V heads of 128): 551 us, 980 TFLOP/s, over a
-// bf16 pool, 642 us over an 8-bit one (its softmax reads the groups' scales and has 4
-// operand buffers instead of 5); without the ranges' ends on the SMs that 128 units leave
-// over, 565 and 655. Per 256 x 128 tile about 4000 clocks: 2048 of
-// MMAs, 2048 of exponentials, and what one softmax warp per row tile and scheduler cannot
-// overlap. A CTA takes about 6 us to start (lengths, pages, Q, first tiles) and end.
+// 1024 queries of 32 heads over 32768 keys (8 K/V heads of 128): 528 us alone, 1020 TFLOP/s,
+// over a bf16 pool (599 replayed 20 times in a row, at the power limit), 612 (621) us over
+// an 8-bit one (its softmax reads the groups' scales, spills
+// some 80 bytes a thread and has 4 operand buffers instead of 5). Per 256 x 128 tile of the
+// latter 4700 clocks (1.067 million of the kernel over 227 tiles): tensor pipe 45 % active,
+// exponential unit 46 %, issue slots 47 %. What neither covers is one softmax warp per row
+// tile and scheduler waiting for its own results; it is not located further. A CTA takes
+// about 6 us to start (lengths, pages, Q, first tiles) and end.
 // 8-bit pools: a group of 16 keys lies in one page, so its K scale is a factor and
 // the exponent of its V scale an offset per 16 scores; the V scale's mantissa (1
 // for the powers of two that the append writes) is multiplied into V's fp16.

@@ -252,7 +252,7 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
 
 // BF16 pool: a block takes `tokens` tokens of one sequence, all heads. A thread keeps
 // its head and chunks and goes from token to token, kAppendAhead of them in flight, so
-// nothing is divided or looked up per unit (3889 tokens of 12 heads of 128: 14.8 us a
+// nothing is divided or looked up per unit (3889 tokens of 12 heads of 128: 14.7 us a
 // call, 10.9 replayed out of a graph; floor 7.3).
 constexpr int kAppendAhead = 2, kAppendMaxTokens = 32;
 
@@ -385,7 +385,7 @@ __device__ __forceinline__ __nv_bfloat162 bf16_amax(const uint4& u, __nv_bfloat1
 // the next heads' loads are issued before this round's barrier. The angles are computed
 // once for all heads of a block. Measured (8800 tokens, 8 heads of 128, pages of 64): a
 // block per head, 65 us; angles shared but two units per thread, so that registers left
-// one block per SM, 42 us; as here 20.8 us, floor 8.2.
+// one block per SM, 42 us; as here 20.7 us, floor 8.2.
 __global__ void __launch_bounds__(kPagedAppendMaxThreads, 1) paged_append_e4m3_kernel(const PagedAppendParams p) {
   extern __shared__ float2 s_cs[];
   __shared__ uint32_t s_max[2][2][kPagedAppendMaxThreads / 32];  // [parity][K, V][warp]: bits of the maximum
