@@ -529,8 +529,8 @@ typedef struct ll_score_desc {
  * Over a BF16 pool the softmax weights are rounded to bf16, and the rotated q to two bf16
  * terms (one where D is 128 and the call has more than a few rows);
  * over an FP8 pool codes are used exactly, q and weights are rounded to fp16
- * under a power-of-two scale (weights below 2^-20 of a row's largest to steps of 2^-30 of it). Sums, maxima and outputs before the last rounding
- * are fp32.
+ * under a power-of-two scale (weights below 2^-20 of a row's largest to steps of
+ * 2^-30 of it). Sums, maxima and outputs before the last rounding are fp32.
  * workspace: ll_paged_attention_workspace_bytes() bytes (NULL allowed when 0),
  * uninitialised, 16-byte aligned; calls that share it must be ordered.
  * Errors: LL_ERR_INVALID_ARG for NULL or misaligned pointers, an invalid cache,

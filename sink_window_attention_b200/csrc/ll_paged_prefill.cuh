@@ -21,9 +21,8 @@
 //    exceeded by 2^8 (2^14 over an 8-bit pool, where it starts 2^6 below the maximum).
 // 1024 queries of 32 heads over 32768 keys (8 K/V heads of 128): 528 us alone, 1020 TFLOP/s,
 // over a bf16 pool (599 replayed 20 times in a row, at the power limit), 612 (621) us over
-// an 8-bit one (its softmax reads the groups' scales, spills
-// some 80 bytes a thread and has 4 operand buffers instead of 5). Per 256 x 128 tile of the
-// latter 4700 clocks (1.067 million of the kernel over 227 tiles): tensor pipe 45 % active,
+// an 8-bit one (its softmax reads the groups' scales, spills some 80 bytes a thread and has
+// 4 operand buffers instead of 5). Per 256 x 128 tile of the latter 4700 clocks (1.067 million of the kernel over 227 tiles): tensor pipe 45 % active,
 // exponential unit 46 %, issue slots 47 %. What neither covers is one softmax warp per row
 // tile and scheduler waiting for its own results; it is not located further. A CTA takes
 // about 6 us to start (lengths, pages, Q, first tiles) and end.
@@ -48,12 +47,12 @@ struct PrefillTraits {
   static constexpr int CTRL = 2048;
   // 8-bit pools: a tile's codes of K and V on their way to fp16
   static constexpr int RAW = E4M3 ? 2 * BN * D : 0;
-  // Terms of a rotated q. One bf16 term is off by 2^-9 of each element, which no V averages
-  // out (output error 3.6e-3 of its norm, two terms 2.3e-3). At D = 64 two more tiles of
-  // 16 KB fit beside the buffers and the second product hides (ragged prompts of 32 heads:
-  // 218 us rotated, 202 not). At D = 128 they would leave 3 of 5 buffers, and the products
-  // would be most of a tile's time: 2 to 3 thousand rows 249 -> 285 us, a chunk of 1024 over
-  // 32768 582 -> 711, so there one term stays. fp16 (8-bit pools) has three bits more in one.
+  // Terms of a rotated q. One bf16 term rounds each element by up to 2^-8 (output error
+  // 3.6e-3 of its norm, with two terms 2.3e-3). At D = 64 two more tiles of 16 KB fit beside
+  // the buffers and the second product hides (ragged prompts of 32 heads: 218 us rotated, 202
+  // not). At D = 128 they would leave 3 of 5 buffers, and the products would be most of a
+  // tile's time: ragged prompts 249 -> 285 us, a chunk of 1024 over 32768 582 -> 711, so
+  // there one term stays. fp16 (8-bit pools) has three bits more in one.
   static constexpr int QS = !E4M3 && D == 64 ? 2 : 1;
   static constexpr int FREE = (232448 - CTRL - 1024 - RAW) / TILE - 2 * QS;
   static constexpr int STAGES = FREE < 8 ? FREE : 8;
